@@ -49,8 +49,12 @@ typedef enum {
   S2ATTN_ERR_UNSUPPORTED = -2,    /* valid, but not a shape this path handles */
   S2ATTN_ERR_WORKSPACE = -3,      /* workspace missing or too small */
   S2ATTN_ERR_CUDA = -4,           /* a CUDA runtime/driver call failed */
-  S2ATTN_ERR_DEVICE_TIMEOUT = -5  /* a kernel gave up on a bounded wait */
+  S2ATTN_ERR_DEVICE_TIMEOUT = -5, /* a kernel gave up on a bounded wait */
+  S2ATTN_ERR_DEVICE_INDEX = -6    /* a length, page, row or parent held on the device is out of range */
 } s2attn_status;
+
+/* Element types of the calls that take a `dtype`. */
+typedef enum { S2ATTN_BF16 = 0, S2ATTN_FP16 = 1, S2ATTN_F32 = 2 } s2attn_dtype;
 
 /* Version of this ABI (major * 100 + minor). */
 int s2attn_version(void);
@@ -193,6 +197,126 @@ int rope_pi_apply_offset(void* q, void* k, int B, int N, int H, int D, int pos0,
                          void* stream);
 
 /*
+ * RMS norm of every q and k head with the rotary embedding, in one pass.  For a head's row x
+ * of D elements at position t (norm != 0; without it y = x):
+ *   y = w * x / sqrt(mean(x^2) + eps)
+ * and the first R elements of y turn in pairs by the angles t * inv_freq[i], i < R/2:
+ *   (a, b) -> attn_factor * (a cos - b sin, b cos + a sin)
+ * with pairs (i, i + R/2), or (2i, 2i + 1) when interleaved != 0; the other D - R pass.
+ *   q, q_out : [B, N, Hq, D]     k, k_out : [B, N, Hk, D]   (q or k with its output may be NULL)
+ *   wq, wk   : [D] weights of dtype, NULL for 1
+ *   positions: [B, N] int32, any value, or NULL: row t of every sequence is at pos0 + t
+ *   inv_freq : [R/2] fp32 frequencies (device), e.g. from rope_inv_freq
+ * dtype: S2ATTN_BF16, S2ATTN_FP16 or S2ATTN_F32.  Sums and products are fp32, angles are formed
+ * and reduced in 64 bits, the result is rounded once.  q_out == q and k_out == k (in place) are
+ * allowed; other overlaps are not.  Requirements: D % 16 == 0, D <= 256; R % 16 == 0,
+ * 0 <= R <= D; eps >= 0; device pointers 16-byte aligned (positions and inv_freq 4-byte).
+ */
+int qk_norm_rope_fwd(const void* q, const void* k, const void* wq, const void* wk, const int* positions,
+                     const float* inv_freq, void* q_out, void* k_out, int B, int N, int Hq, int Hk, int D, int R,
+                     int interleaved, int norm, float eps, float attn_factor, int pos0, int dtype, void* stream);
+
+/*
+ * Backward of qk_norm_rope_fwd: dq, dk (of dtype) from the gradients dq_out, dk_out and the
+ * forward's inputs q, k (not read, and may be NULL, when norm == 0), and dwq, dwk [D] of dtype
+ * (either may be NULL: not wanted; both must be NULL when norm == 0).  dw is the fp32 sum over
+ * all tokens and heads, added in an order that depends on the sizes and the device alone.
+ * dq == dq_out and dk == dk_out are allowed.  `workspace`: device, 256-byte aligned, at
+ * least qk_norm_rope_bwd_workspace_bytes(D) bytes; may be NULL when dwq and dwk are.
+ */
+size_t qk_norm_rope_bwd_workspace_bytes(int D);
+int qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const void* wq,
+                     const void* wk, const int* positions, const float* inv_freq, void* dq, void* dk, void* dwq,
+                     void* dwk, int B, int N, int Hq, int Hk, int D, int R, int interleaved, int norm, float eps,
+                     float attn_factor, int pos0, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary frequencies for a context stretched by `factor` (host arrays; no GPU is used):
+ * inv_freq[0 .. R/2) and *attn_factor.  With f_i = base^(-2i/R):
+ *   scaling 0: f_i.   1 (position interpolation): f_i / factor.
+ *   2 (a larger base): the base becomes base * factor^(R / (R - 2)).
+ *   3 (by wavelength): frequencies that turn more than beta_fast times within original_len
+ *     tokens stay, those below beta_slow are divided by factor, with a linear ramp over i
+ *     between floor(i_fast) and ceil(i_slow), i_n = R ln(original_len / (2 pi n)) / (2 ln base);
+ *     *attn_factor = 0.1 ln(factor) + 1.
+ * *attn_factor is 1 otherwise.  Requirements: R even, 2 <= R <= 256 (R >= 4 for scaling 2);
+ * base > 1; factor >= 1; for scaling 3 original_len >= 1 and beta_fast > beta_slow > 0.
+ */
+int rope_inv_freq(float* inv_freq, float* attn_factor, int R, float base, int scaling, float factor,
+                  int original_len, float beta_fast, float beta_slow);
+
+/*
+ * The paged cache of the calls below.  k_pages and v_pages are pools [n_pages, page_size, Hkv, D];
+ * row b of page_table ([B, table_width] int32) lists the pages of sequence b in order, so
+ * its token t lies in page page_table[b][t / page_size] at row t % page_size.  cache_len ([B]
+ * int32) counts its tokens.  Entries behind the last token's page are never read.
+ * page_size is a power of two >= 16; n_pages * page_size <= 2^31 - 256.
+ * Lengths, pages, rows and parents are read on the device: one that is out of range is
+ * recorded (s2attn_get_device_error returns S2ATTN_ERR_DEVICE_INDEX until cleared) and faults
+ * nothing; the outputs of the sequence that holds it are then unspecified, those of others
+ * are not affected, and later calls run.
+ */
+
+/*
+ * Ancestor masks of trees of drafted tokens: parents [B, M] int32, parents[b][m] < m or -1
+ * for a node that follows the cache directly.  mask [B, M, ceil(M/64)] 64-bit words: bit j%64
+ * of word j/64 of row m is set where j is m or one of its ancestors.  depth ([B, M] int32, may
+ * be NULL): the number of m's ancestors, so that m's position is cache_len + depth.
+ * 1 <= M <= 128 (else S2ATTN_ERR_UNSUPPORTED).  A parent outside [-1, m) is recorded and
+ * read as -1.
+ */
+int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, int B, int M, void* stream);
+
+/*
+ * Attention of M drafted tokens of each sequence over its paged cache and over each other, with
+ * scale 1/sqrt(D): a decoding step for one token (M = 1), several in a row (mask NULL), or a tree.
+ *   q            : [B, M, H, D]; query heads [g*H/Hkv, (g+1)*H/Hkv) use key head g
+ *   k_new, v_new : [B, M, Hkv, D], the drafted tokens' keys and values
+ *   tree_mask    : [B, M, ceil(M/64)] words as above, any bits; NULL: token m sees j <= m
+ *   new_len      : [B] int32 in 0..M, or NULL for M: sequence b has new_len[b] drafted tokens
+ *   o            : [B, M, H, D];  lse: [B, H, M] fp32, natural log of the sum of exp(score)
+ * Token m of sequence b attends to the cache's cache_len[b] tokens and to the drafted tokens
+ * j < new_len[b] whose bit is set in its mask row.  Rows m >= new_len[b] of o and lse are left as
+ * they were.  A token that sees nothing gets o = 0 and lse = -inf.  What is not visible to
+ * a token does not reach it, whatever it holds (infinities and NaN included).
+ * dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to dtype for the
+ * second product.  Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024
+ * (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte aligned, at least
+ * s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the GPU
+ * need one each.  Lengths are read on the device only, so a captured call follows them.  Runs
+ * up to two kernels on `stream`.  The result does not depend on what else runs.
+ */
+size_t s2attn_tree_decode_workspace_bytes(int B, int M, int H, int Hkv, int D);
+int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, const void* k_pages,
+                       const void* v_pages, const int* page_table, const int* cache_len, const int* new_len,
+                       const unsigned long long* tree_mask, void* o, float* lse, int B, int M, int H, int Hkv, int D,
+                       int n_pages, int page_size, int table_width, int dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Writes rows of k_new and v_new ([B, M, Hkv, D]) into the pages of their sequences: for j < n_rows[b],
+ * row rows[b][j] goes to position cache_len[b] + j.  rows [B, A] int32 (any order, repeats allowed);
+ * NULL: row j, A = M.  n_rows [B] int32 (values above A count as A, below 0 as 0); NULL: A.
+ * cache_len is not changed.  elem_size: bytes of an element (2 or 4); Hkv * D * elem_size must be a
+ * multiple of 16.  No two sequences may own the same page at a position that is written.
+ */
+int s2attn_cache_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, const int* page_table,
+                        const int* cache_len, const int* rows, const int* n_rows, int B, int M, int A, int Hkv, int D,
+                        int n_pages, int page_size, int table_width, int elem_size, void* stream);
+
+/*
+ * Copies whole pages inside each of n_pools pools (1 .. 128 device pointers in a host array;
+ * e.g. the K and V pools of every layer): page pairs[2i] to page pairs[2i + 1].  Used to fork a
+ * sequence (its last, partly filled page gets a copy; full pages are shared by the tables) and
+ * to move pages.  pairs is a host array, checked before anything is enqueued: pages in
+ * [0, n_pages), no page written twice, none both read and written (S2ATTN_ERR_INVALID_ARG).
+ * One page may be read several times.  page_bytes: bytes of a page, a multiple of 16.
+ * n_pairs = 0 does nothing.
+ */
+int s2attn_cache_copy_pages(void* const* pools, int n_pools, const int* pairs, int n_pairs, int n_pages,
+                            size_t page_bytes, void* stream);
+
+/*
  * LoRA-adapted linear projections, the steps on either side of S^2-Attn in a LongLoRA
  * layer ("LongLoRA paper notes", section 3.2: low-rank adapters on the Q, K, V and O
  * projections; nearauto.com article, "long-context LoRA improvement").  For `parts`
@@ -279,7 +403,9 @@ int s2attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* 
  * Reads the current device's error word: S2ATTN_OK if no kernel has failed since
  * the last clear, else S2ATTN_ERR_DEVICE_TIMEOUT with *detail (if non-NULL) set to
  * (kernel << 8) | site (kernel 1 = forward, 2 = backward, 4 = decoding step,
- * 5 = LoRA projection).  In the
+ * 5 = LoRA projection, 6 = tree attention and masks, 7 = cache).  An index out of range
+ * (site 0x40) is held in a word of its own, which makes no kernel skip its work: it returns
+ * S2ATTN_ERR_DEVICE_INDEX when no other failure is recorded.  In the
  * bounds-checked build (libs2attn_debug.so, compiled with S2ATTN_DEBUG) a site with bit
  * 0x80 set is a global store or reduction whose computed index fell outside its tensor;
  * the access was skipped.  Synchronize the streams
@@ -287,7 +413,7 @@ int s2attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* 
  */
 int s2attn_get_device_error(int* detail);
 
-/* Resets the current device's error word to 0 (synchronous). */
+/* Resets the current device's error words to 0 (synchronous). */
 int s2attn_clear_device_error(void);
 
 /*

@@ -15,6 +15,9 @@ __all__ = [
     "s2attn_bwd_dq_convert", "s2attn_bwd_noalloc", "s2attn_decode", "s2attn_decode_workspace_bytes", "s2attn_fwd_f32", "s2attn_bwd_f32", "rope_pi_apply", "rope_pi_apply_offset",
     "lora_proj_fwd", "lora_proj_workspace_bytes", "lora_proj_bwd", "lora_proj_bwd_workspace_bytes",
     "s2attn_halo_rows", "s2attn_halo_lse",
+    "rope_inv_freq", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
+    "s2attn_tree_mask", "s2attn_tree_decode", "s2attn_tree_decode_workspace_bytes",
+    "s2attn_cache_append", "s2attn_cache_copy_pages",
     "get_device_error", "clear_device_error", "s2attn_selftest_bounded_wait",
 ]
 
@@ -23,7 +26,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.environ.get("S2ATTN_LIBRARY") or os.path.join(_HERE, "libs2attn.so")
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "workspace", -4: "CUDA error",
-          -5: "device timeout"}
+          -5: "device timeout", -6: "device index out of range"}
 
 
 class S2AttnError(RuntimeError):
@@ -67,6 +70,15 @@ def capi():
         "lora_proj_bwd": ([P, P, P, P, P, P, P, P, I, I, I, I, I, F, P, Z, P], I),
         "s2attn_halo_rows": ([ctypes.POINTER(P), ctypes.POINTER(P), I, I, I, I, I, I, I, I, P], I),
         "s2attn_halo_lse": ([ctypes.POINTER(P), ctypes.POINTER(P), I, I, I, I, I, I, I, P], I),
+        "rope_inv_freq": ([P, P, I, F, I, F, I, F, F], I),
+        "qk_norm_rope_fwd": ([P] * 8 + [I] * 8 + [F, F, I, I, P], I),
+        "qk_norm_rope_bwd_workspace_bytes": ([I], Z),
+        "qk_norm_rope_bwd": ([P] * 12 + [I] * 8 + [F, F, I, I, P, Z, P], I),
+        "s2attn_tree_mask": ([P, P, P, I, I, P], I),
+        "s2attn_tree_decode_workspace_bytes": ([I, I, I, I, I], Z),
+        "s2attn_tree_decode": ([P] * 11 + [I] * 9 + [P, Z, P], I),
+        "s2attn_cache_append": ([P] * 8 + [I] * 9 + [P], I),
+        "s2attn_cache_copy_pages": ([ctypes.POINTER(P), I, ctypes.POINTER(I), I, I, Z, P], I),
         "s2attn_get_device_error": ([ctypes.POINTER(I)], I),
         "s2attn_clear_device_error": ([], I),
         "s2attn_selftest_bounded_wait": ([ctypes.c_uint, P], I),
@@ -381,6 +393,254 @@ def lora_proj_bwd(x, w, lora_a, lora_b, dy, dx, d_lora_a, d_lora_b, parts, scali
         _ptr(x), _ptr(w), _ptr(lora_a), _ptr(lora_b), _ptr(dy), _ptr(dx), _ptr(d_lora_a), _ptr(d_lora_b),
         T, K, n_out, parts, r, float(scaling), _ptr(workspace), workspace.numel() * workspace.element_size(),
         _stream(stream)))
+
+
+# The calls below launch on the device of their tensors, which must be one, whatever the current
+# device is; without a `stream` they take that device's current stream.
+
+def _one_device(**tensors):
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} must be on {dev} like the other tensors")
+    return dev
+
+
+def _call_on(dev, fn, stream, *args):
+    torch = _torch()
+    if torch.cuda.current_device() == dev.index:
+        rc = getattr(capi(), fn)(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(capi(), fn)(*args, _stream(stream))
+    _check(fn, rc)
+
+
+def _dtype_code(t, name, f32):
+    torch = _torch()
+    codes = {torch.bfloat16: 0, torch.float16: 1}
+    if f32:
+        codes[torch.float32] = 2
+    if t.dtype not in codes:
+        raise ValueError(f"{name} must be bf16{', fp16 or fp32' if f32 else ' or fp16'}")
+    return codes[t.dtype]
+
+
+def _shaped(t, name, shape, dtype):
+    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_inv_freq(R, base=10000.0, scaling="none", factor=1.0, original_len=4096, beta_fast=32.0, beta_slow=1.0):
+    """(inv_freq [R/2] fp32 on the host, attn_factor) for a context stretched by `factor`: scaling
+    "none", "linear" (position interpolation), "ntk" (a larger base) or "yarn" (by wavelength)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    if R < 2 or R % 2 or R > 256:
+        raise ValueError("R must be even, 2 to 256")
+    out = _torch().empty(R // 2, dtype=_torch().float32)
+    af = ctypes.c_float(0.0)
+    _check("rope_inv_freq", capi().rope_inv_freq(_ptr(out), ctypes.byref(af), R, base, _SCALINGS[scaling], factor,
+                                                 original_len, beta_fast, beta_slow))
+    return out, af.value
+
+
+def _norm_rope_args(pairs, inv_freq, wq, wk, norm, positions, pos0):
+    """Checks the sides of a call; pairs: [(name, tensor, same-shaped tensors...)] for q and k."""
+    torch = _torch()
+    if all(p[1] is None for p in pairs):
+        raise ValueError("q or k must be given")
+    ref = next(p[1] for p in pairs if p[1] is not None)
+    B, N, _, D = _bnhd(ref, "q/k")
+    for name, t, *others in pairs:
+        if t is None:
+            if any(o is not None for _, o in others):
+                raise ValueError(f"{name} must be given with its output or gradient")
+            continue
+        if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N or t.shape[3] != D:
+            raise ValueError("q and k must be [B,N,H,D] with the same B, N and D")
+        _shaped(t, name, t.shape, ref.dtype)
+        for oname, o in others:
+            _shaped(o, oname, t.shape, ref.dtype)
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            if not norm:
+                raise ValueError(f"{name} is only used with norm=True")
+            _shaped(w, name, (D,), ref.dtype)
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous fp32 vector of R/2 frequencies")
+    if positions is not None:
+        _shaped(positions, "positions", (B, N), torch.int32)
+    if not -2 ** 31 <= pos0 < 2 ** 31 - N:
+        raise ValueError("pos0 is outside the range of positions")
+    heads = [0 if p[1] is None else p[1].shape[2] for p in pairs]
+    return ref, B, N, heads[0], heads[1], D, 2 * inv_freq.numel()
+
+
+def qk_norm_rope_fwd(q, k, q_out, k_out, inv_freq, wq=None, wk=None, norm=True, eps=1e-6, positions=None, pos0=0,
+                     attn_factor=1.0, interleaved=False, stream=None):
+    """RMS norm of every head of q [B,N,Hq,D] and k [B,N,Hk,D] (norm=False: none) and the rotary
+    embedding of its first 2*len(inv_freq) elements, in one pass, into q_out and k_out (which
+    may be q and k).  q with q_out, or k with k_out, may be None.  wq, wk [D] (None: 1);
+    positions [B,N] int32 (None: pos0 + row); bf16, fp16 or fp32."""
+    ref, B, N, Hq, Hk, D, R = _norm_rope_args([("q", q, ("q_out", q_out)), ("k", k, ("k_out", k_out))], inv_freq, wq,
+                                              wk, norm, positions, pos0)
+    dt = _dtype_code(ref, "q/k", True)
+    dev = _one_device(q=q, k=k, q_out=q_out, k_out=k_out, wq=wq, wk=wk, positions=positions, inv_freq=inv_freq)
+    _call_on(dev, "qk_norm_rope_fwd", stream, _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(inv_freq),
+             _ptr(q_out), _ptr(k_out), B, N, Hq, Hk, D, R, int(interleaved), int(norm), eps, attn_factor, pos0, dt)
+
+
+def qk_norm_rope_bwd_workspace_bytes(D):
+    return int(capi().qk_norm_rope_bwd_workspace_bytes(D))
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, inv_freq, wq=None, wk=None, dwq=None, dwk=None, norm=True, eps=1e-6,
+                     positions=None, pos0=0, attn_factor=1.0, interleaved=False, workspace=None, stream=None):
+    """Backward of qk_norm_rope_fwd: dq, dk (which may be dq_out, dk_out) and, where given, dwq, dwk
+    [D].  q, k are the forward's inputs (norm=False: may be None).  workspace: a uint8 device
+    tensor of qk_norm_rope_bwd_workspace_bytes(D) bytes, needed with dwq or dwk."""
+    sides = [("dq_out", dq_out, ("dq", dq)), ("dk_out", dk_out, ("dk", dk))]
+    if norm:
+        for s, name, x in ((0, "q", q), (1, "k", k)):
+            sides[s] += ((name, x),)
+    ref, B, N, Hq, Hk, D, R = _norm_rope_args(sides, inv_freq, wq, wk, norm, positions, pos0)
+    dt = _dtype_code(ref, "q/k", True)
+    for name, d, g in (("dwq", dwq, dq), ("dwk", dwk, dk)):
+        if d is not None:
+            if not norm or g is None:
+                raise ValueError(f"{name} needs norm=True and its side's gradient")
+            _shaped(d, name, (D,), ref.dtype)
+    if dwq is not None or dwk is not None:
+        _workspace(workspace)
+    else:
+        workspace = None
+    if not norm:
+        q = k = None
+    dev = _one_device(q=q, k=k, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk, wq=wq, wk=wk, dwq=dwq, dwk=dwk,
+                      positions=positions, inv_freq=inv_freq, workspace=workspace)
+    _call_on(dev, "qk_norm_rope_bwd", stream, _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(wq), _ptr(wk),
+             _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), B, N, Hq, Hk, D, R,
+             int(interleaved), int(norm), eps, attn_factor, pos0, dt, _ptr(workspace),
+             0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def s2attn_tree_mask(parents, mask, depth=None, stream=None):
+    """Ancestor masks of trees of drafted tokens: parents [B,M] int32 (-1: follows the cache) ->
+    mask [B,M,ceil(M/64)] int64 (bit j: j is m or an ancestor) and depth [B,M] int32."""
+    torch = _torch()
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B,M]")
+    B, M = parents.shape
+    _shaped(parents, "parents", (B, M), torch.int32)
+    _shaped(mask, "mask", (B, M, (M + 63) // 64), torch.int64)
+    if depth is not None:
+        _shaped(depth, "depth", (B, M), torch.int32)
+    dev = _one_device(parents=parents, mask=mask, depth=depth)
+    _call_on(dev, "s2attn_tree_mask", stream, _ptr(parents), _ptr(mask), _ptr(depth), B, M)
+
+
+def s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D):
+    return int(capi().s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D))
+
+
+def _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype):
+    torch = _torch()
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_pages must be [n_pages,page_size,Hkv,D] and page_table [B,table_width]")
+    n_pages, page_size = k_pages.shape[:2]
+    _shaped(k_pages, "k_pages", (n_pages, page_size, Hkv, D), dtype)
+    _shaped(v_pages, "v_pages", (n_pages, page_size, Hkv, D), dtype)
+    _shaped(page_table, "page_table", (B, page_table.shape[1]), torch.int32)
+    _shaped(cache_len, "cache_len", (B,), torch.int32)
+    return n_pages, page_size, page_table.shape[1]
+
+
+def s2attn_tree_decode(q, k_new, v_new, k_pages, v_pages, page_table, cache_len, o, lse, workspace, tree_mask=None,
+                       new_len=None, stream=None):
+    """Attention of drafted tokens (q [B,M,H,D], k_new, v_new [B,M,Hkv,D]) over the paged cache
+    (k_pages, v_pages [n_pages,page_size,Hkv,D], page_table [B,width] and cache_len [B] int32) and
+    over each other by tree_mask [B,M,ceil(M/64)] int64 (None: token m sees j <= m), into o like q
+    and lse [B,H,M] fp32.  new_len [B] int32: drafted tokens of each sequence (None: M); the
+    other rows of o and lse stay.  bf16 or fp16.  workspace: a uint8 device tensor of
+    s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D) bytes, one per call in flight."""
+    torch = _torch()
+    B, M, H, D = _bnhd(q, "q")
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [B,M,Hkv,D]")
+    Hkv = k_new.shape[2]
+    dt = _dtype_code(q, "q", False)
+    _shaped(k_new, "k_new", (B, M, Hkv, D), q.dtype)
+    _shaped(v_new, "v_new", (B, M, Hkv, D), q.dtype)
+    n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, q.dtype)
+    _shaped(o, "o", (B, M, H, D), q.dtype)
+    _shaped(lse, "lse", (B, H, M), torch.float32)
+    if tree_mask is not None:
+        _shaped(tree_mask, "tree_mask", (B, M, (M + 63) // 64), torch.int64)
+    if new_len is not None:
+        _shaped(new_len, "new_len", (B,), torch.int32)
+    _workspace(workspace)
+    dev = _one_device(q=q, k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
+                      cache_len=cache_len, o=o, lse=lse, tree_mask=tree_mask, new_len=new_len, workspace=workspace)
+    _call_on(dev, "s2attn_tree_decode", stream, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
+             _ptr(page_table), _ptr(cache_len), _ptr(new_len), _ptr(tree_mask), _ptr(o), _ptr(lse), B, M, H, Hkv, D,
+             n_pages, page_size, width, dt, _ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def s2attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, rows=None, n_rows=None, stream=None):
+    """Writes rows of k_new, v_new [B,M,Hkv,D] into the sequences' pages: for j < n_rows[b] row
+    rows[b][j] goes to position cache_len[b] + j.  rows [B,A] int32 (None: row j, all M);
+    n_rows [B] int32 (None: A).  cache_len is not changed.  bf16, fp16 or fp32."""
+    torch = _torch()
+    B, M, Hkv, D = _bnhd(k_new, "k_new")
+    _dtype_code(k_new, "k_new", True)
+    _shaped(v_new, "v_new", (B, M, Hkv, D), k_new.dtype)
+    n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, k_new.dtype)
+    A = M
+    if rows is not None:
+        if rows.dim() != 2:
+            raise ValueError("rows must be [B,A]")
+        A = rows.shape[1]
+        _shaped(rows, "rows", (B, A), torch.int32)
+    if n_rows is not None:
+        _shaped(n_rows, "n_rows", (B,), torch.int32)
+    dev = _one_device(k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
+                      cache_len=cache_len, rows=rows, n_rows=n_rows)
+    _call_on(dev, "s2attn_cache_append", stream, _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
+             _ptr(page_table), _ptr(cache_len), _ptr(rows), _ptr(n_rows), B, M, A, Hkv, D, n_pages, page_size, width,
+             k_new.element_size())
+
+
+def s2attn_cache_copy_pages(pools, pairs, stream=None):
+    """Copies pages inside every tensor of `pools` ([n_pages, page_size, Hkv, D], one shape and dtype,
+    at most 128): for (src, dst) in pairs (host integers) page src to page dst.  No page may be
+    written twice, or both read and written."""
+    if not pools:
+        raise ValueError("pools must be a non-empty list")
+    ref = pools[0]
+    if ref.dim() < 2:
+        raise ValueError("a pool must be [n_pages, ...]")
+    for i, t in enumerate(pools):
+        _shaped(t, f"pools[{i}]", ref.shape, ref.dtype)
+    dev = _one_device(**{f"pools[{i}]": t for i, t in enumerate(pools)})
+    n_pages = ref.shape[0]
+    flat = []
+    for src, dst in pairs:
+        if not (0 <= src < n_pages and 0 <= dst < n_pages):
+            raise ValueError(f"pair ({src}, {dst}) is outside [0, {n_pages})")
+        flat += (int(src), int(dst))
+    _call_on(dev, "s2attn_cache_copy_pages", stream, _ptr_array(pools), len(pools), (ctypes.c_int * len(flat))(*flat),
+             len(pairs), n_pages, ref.numel() // max(n_pages, 1) * ref.element_size())
+
 
 
 def get_device_error():

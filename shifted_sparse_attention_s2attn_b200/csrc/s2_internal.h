@@ -10,7 +10,9 @@ namespace s2 {
 
 // Device error codes (first failure wins; read with s2attn_get_device_error).
 // code = (kernel << 8) | site
-enum Kernel : int { K_FWD = 1, K_BWD = 2, K_SELFTEST = 3, K_DEC = 4, K_LORA = 5 };
+enum Kernel : int { K_FWD = 1, K_BWD = 2, K_SELFTEST = 3, K_DEC = 4, K_LORA = 5, K_TREE = 6, K_CACHE = 7 };
+// Site of an index word: a length, page, row or parent held on the device lies outside its range.
+constexpr int SITE_INDEX = 0x40;
 
 // Argument rules of the bf16 tensor-core entry points (shape, D == 128, tile alignment of G and
 // G/2, and the index-overflow guards): S2ATTN_OK or the status those entry points return.
@@ -115,5 +117,59 @@ cudaError_t launch_halo_lse(float* const* x, float* const* buf, int n, int to_bu
 // RoPE-PI in place on bf16 q and k, with a cos/sin table [N, D/2] (fp32 each).
 cudaError_t launch_rope_pi(void* q, void* k, const float* cos_tab, const float* sin_tab, int B, int N, int H,
                            int D, cudaStream_t st);
+
+// RMS norm of q and k heads with the rotary embedding (s2attn_norm_rope.cu).  Forward: q_dst,
+// k_dst are the outputs; backward: the gradients dq, dk from dq_out, dk_out.  Either side is
+// left out when its destination is NULL.
+struct NormRopeArgs {
+  const void *q, *k, *dq_out, *dk_out, *wq, *wk;
+  void *q_dst, *k_dst, *dwq, *dwk;
+  const int* positions;    // [B, N] or NULL: pos0 + t
+  const float* inv_freq;   // [R/2]
+  int B, N, Hq, Hk, D, R, pos0, interleaved, norm, dtype;
+  float eps, attn_factor;
+};
+constexpr int kNormRopePartials = 1024;   // rows of the backward's partial sums, at most
+cudaError_t launch_norm_rope_fwd(const NormRopeArgs& a, int n_sm, cudaStream_t st);
+cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* part, int n_sm, cudaStream_t st);
+
+// Attention of drafted tokens over a paged cache (s2attn_tree_sm100.cu) and their masks.
+constexpr int kTreeMaxM = 128;
+constexpr int kTreeMaxB = 1024;           // lengths held in shared memory
+constexpr int kTreeSlots = 2 * 148;       // two CTAs on each SM of a B200
+constexpr int kTreeMinRun = 2;            // key tiles of a run, at least
+struct TreePlan {
+  int group;      // query heads of a key head
+  int tok;        // drafted tokens of a 128-row tile
+  int RT;         // row tiles
+  int J;          // runs a unit's key tiles are cut into
+  int slot_rows;  // rows of a partial
+};
+struct TreeMaps {
+  CUtensorMap q, k_pages, v_pages, k_new, v_new;
+};
+struct TreeArgs {
+  void* o;
+  float *lse, *part_o, *part_ml;
+  int* meta;
+  const int *cache_len, *new_len, *page_table;
+  const unsigned long long* mask;
+  const void* v_new;
+  int B, M, H, Hkv, D, page_shift, n_pages, width, dtype;
+  int *err, *index_err;
+};
+TreePlan tree_plan(int M, int H, int Hkv);
+cudaError_t launch_tree_decode(const TreeMaps& maps, const TreeArgs& a, const TreePlan& t, cudaStream_t st);
+cudaError_t launch_tree_mask(const int* parents, unsigned long long* mask, int* depth, int B, int M, int* index_err,
+                             cudaStream_t st);
+
+// Paged cache (s2attn_cache.cu): new rows to their pages; page copies inside pools.
+constexpr int kCacheMaxPools = 128;
+constexpr int kCacheCopyPairs = 448;      // page pairs of one launch
+cudaError_t launch_cache_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, const int* table,
+                                const int* len, const int* rows, const int* n_rows, int B, int M, int A, int width,
+                                int n_pages, int page_shift, int row_bytes, int* index_err, cudaStream_t st);
+cudaError_t launch_cache_copy(void* const* pools, int n_pools, const int* pairs, int n_pairs, long long page_bytes,
+                              cudaStream_t st);
 
 }  // namespace s2

@@ -2,12 +2,14 @@
 // construction, the RoPE table cache, the device error word, and kernel launches.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <new>
 #include <tuple>
 #include <vector>
 
@@ -17,7 +19,9 @@
 
 namespace {
 
-__device__ int g_error_word;
+// [0]: the first failure inside a kernel (later kernels skip their work while it is set);
+// [1]: the first index out of range (recorded only).
+__device__ int g_error_word[2];
 
 constexpr int kMaxDevices = 64;
 
@@ -230,6 +234,82 @@ size_t decode_part_o_bytes(int B, int M, int N, int H, int D) {
   return align256((size_t)B * H * decode_max_splits(N) * M * D * sizeof(float));
 }
 
+// ---- rotary norm, tree attention, paged cache ---------------------------------------
+bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int check_norm_rope(const s2::NormRopeArgs& a, bool bwd) {
+  if (a.B < 1 || a.N < 1 || a.D < 16 || a.D % 16 != 0 || a.D > 256) return S2ATTN_ERR_INVALID_ARG;
+  if (a.R < 0 || a.R > a.D || a.R % 16 != 0) return S2ATTN_ERR_INVALID_ARG;
+  if (a.dtype != S2ATTN_BF16 && a.dtype != S2ATTN_FP16 && a.dtype != S2ATTN_F32) return S2ATTN_ERR_INVALID_ARG;
+  if (!a.q_dst && !a.k_dst) return S2ATTN_ERR_INVALID_ARG;
+  if ((long long)a.B * a.N > INT_MAX / 2) return S2ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(a.eps) || a.eps < 0.f || !std::isfinite(a.attn_factor)) return S2ATTN_ERR_INVALID_ARG;
+  if (a.R > 0 && !aligned4(a.inv_freq)) return S2ATTN_ERR_INVALID_ARG;
+  if (a.positions && !aligned4(a.positions)) return S2ATTN_ERR_INVALID_ARG;
+  if (!a.positions && (long long)a.pos0 + a.N > INT_MAX) return S2ATTN_ERR_INVALID_ARG;
+  const void* src[2] = {a.q, a.k};
+  const void* grad[2] = {a.dq_out, a.dk_out};
+  const void* w[2] = {a.wq, a.wk};
+  void* dst[2] = {a.q_dst, a.k_dst};
+  void* dw[2] = {a.dwq, a.dwk};
+  const int H[2] = {a.Hq, a.Hk};
+  for (int i = 0; i < 2; ++i) {
+    if ((w[i] && !a.norm) || (dw[i] && (!a.norm || !dst[i]))) return S2ATTN_ERR_INVALID_ARG;
+    if (dw[i] && !aligned4(dw[i])) return S2ATTN_ERR_INVALID_ARG;
+    if (!dst[i]) {
+      if (src[i] && !bwd) return S2ATTN_ERR_INVALID_ARG;   // an input without its output
+      continue;
+    }
+    if (H[i] < 1 || H[i] > 65536) return S2ATTN_ERR_INVALID_ARG;
+    if (!aligned16(dst[i]) || (w[i] && !aligned16(w[i]))) return S2ATTN_ERR_INVALID_ARG;
+    if ((!bwd || a.norm) && !aligned16(src[i])) return S2ATTN_ERR_INVALID_ARG;
+    if (bwd && !aligned16(grad[i])) return S2ATTN_ERR_INVALID_ARG;
+  }
+  return S2ATTN_OK;
+}
+
+// log2 of a page size, or -1.
+int page_shift_of(int page_size) {
+  if (page_size < 16 || (page_size & (page_size - 1)) != 0) return -1;
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+int check_pages(int n_pages, int page_size, int table_width) {
+  if (n_pages < 1 || page_size < 1 || table_width < 1) return S2ATTN_ERR_INVALID_ARG;
+  if (page_shift_of(page_size) < 0) return S2ATTN_ERR_UNSUPPORTED;
+  if ((long long)n_pages * page_size > (long long)INT_MAX - 255) return S2ATTN_ERR_UNSUPPORTED;
+  return S2ATTN_OK;
+}
+
+int check_tree_shape(int B, int M, int H, int Hkv, int D) {
+  if (B < 1 || M < 1 || H < 1 || Hkv < 1 || D < 1 || H % Hkv != 0) return S2ATTN_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || M > s2::kTreeMaxM || B > s2::kTreeMaxB || H / Hkv > 128) return S2ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * M * H > INT_MAX) return S2ATTN_ERR_UNSUPPORTED;
+  return S2ATTN_OK;
+}
+
+// A [rows, H, D] 16-bit tensor; a box is box_rows rows of box_heads heads, 64 columns.
+bool map_heads(CUtensorMap* m, const void* base, int dtype, long long rows, int H, int D, int box_heads,
+               int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt =
+      dtype == S2ATTN_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Partials of a tree attention call: outputs, then (max, sum) pairs; then the runs of each
+// (sequence, row tile).
+size_t tree_part_rows(const s2::TreePlan& t, int Hkv) { return (size_t)Hkv * t.RT * t.J * 2 * t.slot_rows; }
+
 }  // namespace
 
 namespace s2 {
@@ -250,6 +330,7 @@ const char* s2attn_status_string(int status) {
     case S2ATTN_ERR_WORKSPACE: return "workspace missing or too small";
     case S2ATTN_ERR_CUDA: return "CUDA call failed";
     case S2ATTN_ERR_DEVICE_TIMEOUT: return "device-side wait timed out";
+    case S2ATTN_ERR_DEVICE_INDEX: return "device-side index out of range";
     default: return "unknown status";
   }
 }
@@ -580,6 +661,179 @@ int lora_proj_bwd(const void* x, const void* w, const void* lora_a, const void* 
                                          d_lora_a, d_lora_b, T, K, n_out, parts, r, scaling, sm_count(), err, st));
 }
 
+int qk_norm_rope_fwd(const void* q, const void* k, const void* wq, const void* wk, const int* positions,
+                     const float* inv_freq, void* q_out, void* k_out, int B, int N, int Hq, int Hk, int D, int R,
+                     int interleaved, int norm, float eps, float attn_factor, int pos0, int dtype, void* stream) {
+  s2::NormRopeArgs a{};
+  a.q = q, a.k = k, a.wq = wq, a.wk = wk, a.positions = positions, a.inv_freq = inv_freq;
+  a.q_dst = q_out, a.k_dst = k_out;
+  a.B = B, a.N = N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.R = R, a.pos0 = pos0;
+  a.interleaved = interleaved ? 1 : 0, a.norm = norm ? 1 : 0, a.dtype = dtype, a.eps = eps, a.attn_factor = attn_factor;
+  const int rc = check_norm_rope(a, false);
+  if (rc) return rc;
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return S2ATTN_ERR_CUDA;
+  return cuda_status(s2::launch_norm_rope_fwd(a, n_sm, static_cast<cudaStream_t>(stream)));
+}
+
+size_t qk_norm_rope_bwd_workspace_bytes(int D) {
+  if (D < 16 || D % 16 != 0 || D > 256) return 0;
+  return align256((size_t)s2::kNormRopePartials * D * sizeof(float));
+}
+
+int qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const void* wq,
+                     const void* wk, const int* positions, const float* inv_freq, void* dq, void* dk, void* dwq,
+                     void* dwk, int B, int N, int Hq, int Hk, int D, int R, int interleaved, int norm, float eps,
+                     float attn_factor, int pos0, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  s2::NormRopeArgs a{};
+  a.q = q, a.k = k, a.dq_out = dq_out, a.dk_out = dk_out, a.wq = wq, a.wk = wk;
+  a.positions = positions, a.inv_freq = inv_freq;
+  a.q_dst = dq, a.k_dst = dk, a.dwq = dwq, a.dwk = dwk;
+  a.B = B, a.N = N, a.Hq = Hq, a.Hk = Hk, a.D = D, a.R = R, a.pos0 = pos0;
+  a.interleaved = interleaved ? 1 : 0, a.norm = norm ? 1 : 0, a.dtype = dtype, a.eps = eps, a.attn_factor = attn_factor;
+  const int rc = check_norm_rope(a, true);
+  if (rc) return rc;
+  if ((dwq || dwk) && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                       workspace_bytes < qk_norm_rope_bwd_workspace_bytes(D)))
+    return S2ATTN_ERR_WORKSPACE;
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return S2ATTN_ERR_CUDA;
+  return cuda_status(s2::launch_norm_rope_bwd(a, static_cast<float*>(workspace), n_sm, static_cast<cudaStream_t>(stream)));
+}
+
+int rope_inv_freq(float* inv_freq, float* attn_factor, int R, float base, int scaling, float factor,
+                  int original_len, float beta_fast, float beta_slow) {
+  if (!inv_freq || !attn_factor || R < 2 || R % 2 != 0 || R > 256) return S2ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(base) || !(base > 1.f) || !std::isfinite(factor) || !(factor >= 1.f)) return S2ATTN_ERR_INVALID_ARG;
+  if (scaling < 0 || scaling > 3 || (scaling == 2 && R < 4)) return S2ATTN_ERR_INVALID_ARG;
+  if (scaling == 3 && (original_len < 1 || !std::isfinite(beta_fast) || !(beta_slow > 0.f) || !(beta_fast > beta_slow)))
+    return S2ATTN_ERR_INVALID_ARG;
+  double b = base;
+  if (scaling == 2) b *= std::pow((double)factor, (double)R / (R - 2));
+  double low = 0, high = 0;
+  if (scaling == 3) {
+    const double turns = R / (2 * std::log((double)base));
+    low = std::max(0.0, std::floor(turns * std::log(original_len / (2 * M_PI * beta_fast))));
+    high = std::min(R / 2 - 1.0, std::ceil(turns * std::log(original_len / (2 * M_PI * beta_slow))));
+  }
+  for (int i = 0; i < R / 2; ++i) {
+    double f = std::pow(b, -2.0 * i / R);
+    if (scaling == 1) f /= factor;
+    if (scaling == 3) {
+      // a ramp of no width is a step behind `low`
+      const double ramp = std::min(1.0, std::max(0.0, (i - low) / std::max(high - low, 0.001)));
+      f = f / factor * ramp + f * (1.0 - ramp);
+    }
+    inv_freq[i] = (float)f;
+  }
+  *attn_factor = scaling == 3 ? (float)(0.1 * std::log((double)factor) + 1.0) : 1.0f;
+  return S2ATTN_OK;
+}
+
+int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, int B, int M, void* stream) {
+  if (B < 1 || M < 1 || (long long)B * M > INT_MAX) return S2ATTN_ERR_INVALID_ARG;
+  if (M > s2::kTreeMaxM) return S2ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(parents) || !mask || (reinterpret_cast<uintptr_t>(mask) & 7u) || (depth && !aligned4(depth)))
+    return S2ATTN_ERR_INVALID_ARG;
+  int* err = error_word_ptr();
+  if (!err) return S2ATTN_ERR_CUDA;
+  return cuda_status(s2::launch_tree_mask(parents, mask, depth, B, M, err + 1, static_cast<cudaStream_t>(stream)));
+}
+
+size_t s2attn_tree_decode_workspace_bytes(int B, int M, int H, int Hkv, int D) {
+  if (check_tree_shape(B, M, H, Hkv, D)) return 0;
+  const s2::TreePlan t = s2::tree_plan(M, H, Hkv);
+  const size_t rows = tree_part_rows(t, Hkv);
+  return align256(rows * D * sizeof(float)) + align256(rows * 2 * sizeof(float)) +
+         align256((size_t)B * t.RT * 2 * sizeof(int));
+}
+
+int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, const void* k_pages,
+                       const void* v_pages, const int* page_table, const int* cache_len, const int* new_len,
+                       const unsigned long long* tree_mask, void* o, float* lse, int B, int M, int H, int Hkv, int D,
+                       int n_pages, int page_size, int table_width, int dtype, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  int rc = check_tree_shape(B, M, H, Hkv, D);
+  if (rc) return rc;
+  if ((rc = check_pages(n_pages, page_size, table_width))) return rc;
+  if (dtype != S2ATTN_BF16 && dtype != S2ATTN_FP16) return S2ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned16(o) || !aligned4(lse) || !aligned4(page_table) || !aligned4(cache_len))
+    return S2ATTN_ERR_INVALID_ARG;
+  if ((new_len && !aligned4(new_len)) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)) return S2ATTN_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return S2ATTN_ERR_WORKSPACE;
+  int* err = error_word_ptr();
+  if (!err) return S2ATTN_ERR_CUDA;
+  const s2::TreePlan t = s2::tree_plan(M, H, Hkv);
+  const size_t rows = tree_part_rows(t, Hkv);
+  char* ws = static_cast<char*>(workspace);
+  s2::TreeArgs a{};
+  a.o = o, a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float*>(ws + align256(rows * D * sizeof(float)));
+  a.meta = reinterpret_cast<int*>(ws + align256(rows * D * sizeof(float)) + align256(rows * 2 * sizeof(float)));
+  a.cache_len = cache_len, a.new_len = new_len, a.page_table = page_table, a.mask = tree_mask, a.v_new = v_new;
+  a.B = B, a.M = M, a.H = H, a.Hkv = Hkv, a.D = D, a.page_shift = page_shift_of(page_size);
+  a.n_pages = n_pages, a.width = table_width, a.dtype = dtype, a.err = err, a.index_err = err + 1;
+  const int page_box = page_size < 64 ? page_size : 64, new_box = M < 64 ? M : 64;
+  s2::TreeMaps maps;
+  if (!map_heads(&maps.q, q, dtype, (long long)B * M, H, D, t.group, t.tok < M ? t.tok : M) ||
+      !map_heads(&maps.k_pages, k_pages, dtype, (long long)n_pages * page_size, Hkv, D, 1, page_box) ||
+      !map_heads(&maps.v_pages, v_pages, dtype, (long long)n_pages * page_size, Hkv, D, 1, page_box) ||
+      !map_heads(&maps.k_new, k_new, dtype, (long long)B * M, Hkv, D, 1, new_box) ||
+      !map_heads(&maps.v_new, v_new, dtype, (long long)B * M, Hkv, D, 1, new_box))
+    return S2ATTN_ERR_CUDA;
+  return cuda_status(s2::launch_tree_decode(maps, a, t, static_cast<cudaStream_t>(stream)));
+}
+
+int s2attn_cache_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, const int* page_table,
+                        const int* cache_len, const int* rows, const int* n_rows, int B, int M, int A, int Hkv, int D,
+                        int n_pages, int page_size, int table_width, int elem_size, void* stream) {
+  if (B < 1 || M < 1 || A < 1 || Hkv < 1 || D < 1) return S2ATTN_ERR_INVALID_ARG;
+  if (!rows && A != M) return S2ATTN_ERR_INVALID_ARG;
+  if (elem_size != 2 && elem_size != 4) return S2ATTN_ERR_INVALID_ARG;
+  int rc = check_pages(n_pages, page_size, table_width);
+  if (rc) return rc;
+  const long long row_bytes = (long long)Hkv * D * elem_size;
+  if (row_bytes % 16 != 0 || row_bytes > (1 << 20)) return S2ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * M > INT_MAX / 2 || (long long)B * A > INT_MAX / 2) return S2ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned4(page_table) ||
+      !aligned4(cache_len) || (rows && !aligned4(rows)) || (n_rows && !aligned4(n_rows)))
+    return S2ATTN_ERR_INVALID_ARG;
+  int* err = error_word_ptr();
+  if (!err) return S2ATTN_ERR_CUDA;
+  return cuda_status(s2::launch_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, rows, n_rows, B, M,
+                                             A, table_width, n_pages, page_shift_of(page_size), (int)row_bytes, err + 1,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int s2attn_cache_copy_pages(void* const* pools, int n_pools, const int* pairs, int n_pairs, int n_pages,
+                            size_t page_bytes, void* stream) {
+  if (!pools || n_pools < 1 || n_pools > s2::kCacheMaxPools || n_pairs < 0 || n_pages < 1 || page_bytes == 0)
+    return S2ATTN_ERR_INVALID_ARG;
+  if (page_bytes % 16 != 0 || page_bytes > ((size_t)1 << 40)) return S2ATTN_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_pools; ++i)
+    if (!aligned16(pools[i])) return S2ATTN_ERR_INVALID_ARG;
+  if (n_pairs == 0) return S2ATTN_OK;
+  if (!pairs || n_pairs > n_pages) return S2ATTN_ERR_INVALID_ARG;   // each pair writes a page of its own
+  int* dst = new (std::nothrow) int[n_pairs];
+  if (!dst) return S2ATTN_ERR_INVALID_ARG;
+  bool ok = true;
+  for (int i = 0; i < n_pairs; ++i) {
+    ok = ok && pairs[2 * i] >= 0 && pairs[2 * i] < n_pages && pairs[2 * i + 1] >= 0 && pairs[2 * i + 1] < n_pages;
+    dst[i] = pairs[2 * i + 1];
+  }
+  std::sort(dst, dst + n_pairs);
+  for (int i = 1; i < n_pairs; ++i) ok = ok && dst[i] != dst[i - 1];
+  for (int i = 0; i < n_pairs; ++i) ok = ok && !std::binary_search(dst, dst + n_pairs, pairs[2 * i]);
+  delete[] dst;
+  if (!ok) return S2ATTN_ERR_INVALID_ARG;
+  return cuda_status(s2::launch_cache_copy(pools, n_pools, pairs, n_pairs, (long long)page_bytes,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
 int s2attn_selftest_bounded_wait(unsigned timeout_us, void* stream) {
   if (timeout_us == 0 || timeout_us > 1000000u) return S2ATTN_ERR_INVALID_ARG;
   int* err = error_word_ptr();
@@ -589,15 +843,15 @@ int s2attn_selftest_bounded_wait(unsigned timeout_us, void* stream) {
 }
 
 int s2attn_get_device_error(int* detail) {
-  int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(int)) != cudaSuccess) return S2ATTN_ERR_CUDA;
-  if (detail) *detail = v;
-  return v == 0 ? S2ATTN_OK : S2ATTN_ERR_DEVICE_TIMEOUT;
+  int v[2] = {0, 0};
+  if (cudaMemcpyFromSymbol(v, g_error_word, sizeof(v)) != cudaSuccess) return S2ATTN_ERR_CUDA;
+  if (detail) *detail = v[0] ? v[0] : v[1];
+  return v[0] ? S2ATTN_ERR_DEVICE_TIMEOUT : v[1] ? S2ATTN_ERR_DEVICE_INDEX : S2ATTN_OK;
 }
 
 int s2attn_clear_device_error(void) {
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_error_word, &zero, sizeof(int)) == cudaSuccess ? S2ATTN_OK : S2ATTN_ERR_CUDA;
+  const int zero[2] = {0, 0};
+  return cudaMemcpyToSymbol(g_error_word, zero, sizeof(zero)) == cudaSuccess ? S2ATTN_OK : S2ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

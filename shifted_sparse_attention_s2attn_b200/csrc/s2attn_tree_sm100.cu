@@ -1,0 +1,827 @@
+// s2attn_tree_sm100.cu -- attention of drafted tokens over a paged cache (sm_100a).
+//
+// A decoding step checks M drafted tokens of each of B sequences at once.  Query m of
+// sequence b sees every one of the cache's len[b] tokens and those drafted tokens j whose
+// bit is set in row m of a mask (a tree's ancestors; without a mask j <= m):
+//   o_m = sum_j softmax_j(q_m . k_j / sqrt(D)) v_j
+// H query heads share Hkv key heads in groups of `group`, so one key head serves
+// M * group query rows: rows (m, g) of up to 128 / group tokens make a 128-row tile of
+// the tensor cores' M dimension.
+//
+// The step reads 2 * len * Hkv * D elements of K and V once and does 4 * D flops an
+// element pair and row: bound by HBM up to about a hundred rows a key head, by the tensor
+// and exponential units beyond.  The layout follows from the first case:
+//   * unit = (key head, row tile); its work is the concatenation of all sequences' key
+//     tiles (64 keys: first the cache's, then the drafted ones).  J CTAs share a unit and
+//     each takes an equal run of that concatenation, found on the device from len: no
+//     length is needed on the host (a captured graph follows growing sequences), and
+//     sequences of any mix of lengths load every CTA alike.  A run covers the end of one
+//     sequence, whole ones, and the start of another ("segments"); a sequence that lies in
+//     one run is written out at once, one that spans runs leaves a partial (max, sum,
+//     unnormalised output) per run, at most two per CTA, for the combine kernel.
+//   * CTAs of the same run and different heads are neighbours in the grid, so that the
+//     heads of a token are read at about the same time and DRAM pages are read in full.
+//   * K and V stream by TMA, each through a ring and from a warp of its own; a page of at
+//     least 64 tokens is one box per 64 columns, smaller pages one box each.
+//   * S = Q K^T in TMEM, the softmax's P written back over S in 16 bits, O += P V from TMEM;
+//     S(i) is issued before P(i-1) V(i-1), so the softmax of a tile overlaps the product of
+//     the next.  Two CTAs share an SM.
+// P is rounded to the input's 16-bit type (the tensor cores take both operands in one type);
+// its sum is kept from the unrounded fp32 values.  Scores, maxima, sums and O are fp32.
+//
+// Keys that nobody may see are never multiplied: V rows behind the last token of a tile are
+// zeroed in shared memory (0 * NaN is NaN), and a drafted V row that holds infinities or NaN
+// reaches only the rows whose mask shows it (its elements are zeroed for the product and
+// added back to those rows).
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "s2_internal.h"
+#include "s2_ptx.cuh"
+#include "s2attn.h"
+
+namespace s2 {
+namespace tree {
+
+constexpr int BM = 128, BN = 64;
+constexpr int KST = 2, VST = 2;              // ring stages
+constexpr int NTHREADS = 224;
+constexpr int WARP_K = 4, WARP_V = 5, WARP_MMA = 6;
+constexpr uint32_t QBOX = BM * 128;          // 128 rows x 128 B (64 columns)
+constexpr uint32_t KBOX = BN * 128;
+constexpr int NBARS = 2 + 2 * KST + 2 * VST + 2 + 2 + 5;
+constexpr uint32_t TM_COLS = 256;
+constexpr uint32_t TM_O = 128;               // S buffers at columns 0 and 64
+
+template <int HD>
+struct Cfg {
+  static constexpr int NB = HD / 64;         // 64-column boxes of a row
+  static constexpr uint32_t QTILE = NB * QBOX, KTILE = NB * KBOX;
+  static constexpr uint32_t OFF_K = QTILE;
+  static constexpr uint32_t OFF_V = OFF_K + KST * KTILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + VST * KTILE;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + NBARS * 8;   // tmem address, abort flag, run
+  static constexpr uint32_t OFF_LEN = OFF_MISC + 128;         // int len[kTreeMaxB], then new[kTreeMaxB]
+  static constexpr uint32_t SMEM = OFF_LEN + 2 * kTreeMaxB * 4;
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs must fit on an SM");
+};
+
+struct Params {
+  void* o;
+  float* lse;
+  float* part_o;     // [U * J][2][slot_rows][HD]
+  float* part_ml;    // [U * J][2][slot_rows][2]
+  int* meta;         // [B * RT][2]: first and last run of a sequence
+  const int* len;
+  const int* new_len;
+  const int* table;
+  const unsigned long long* mask;
+  const void* v_new;
+  int B, M, H, Hkv, group, RT, tok, J, slot_rows;
+  int page_shift, n_pages, width, words;
+  float sl2;         // log2(e) / sqrt(D)
+  int* err;
+  int* index_err;
+};
+
+enum Site : int { SITE_LOAD = 1, SITE_MMA = 2, SITE_SOFTMAX = 3, SITE_DRAIN = 4, SITE_ALIGN = 5, SITE_STORE = 6 };
+
+__device__ __forceinline__ int cap_tokens(const Params& p) {
+  const long long c = (long long)p.width << p.page_shift;
+  return c > 0x7fffff00LL ? 0x7fffff00 : (int)c;
+}
+
+// Key tiles of the cache, and of the drafted tokens, that sequence b contributes.
+__device__ __forceinline__ int cache_tiles(int len) { return (int)(((long long)len + BN - 1) / BN); }
+__device__ __forceinline__ int all_tiles(int len, int nw, int first_tok) {
+  return nw > first_tok ? cache_tiles(len) + (nw + BN - 1) / BN : 0;
+}
+
+// Walks the segments of a run: `b` and its tiles [t0, t0 + n) of `total`.
+struct Segments {
+  const int* len;
+  const int* nw;
+  int first_tok, b, t0, n, total, left;
+  __device__ __forceinline__ Segments(const int* len_, const int* nw_, int first, int b_, int t_, int left_)
+      : len(len_), nw(nw_), first_tok(first), b(b_), t0(t_), n(0), total(0), left(left_) {}
+  __device__ __forceinline__ bool next() {
+    if (n) {       // leave the current segment
+      ++b;
+      t0 = 0;
+    }
+    if (left <= 0) return false;
+    while ((total = all_tiles(len[b], nw[b], first_tok)) == 0) ++b;
+    n = min(left, total - t0);
+    left -= n;
+    return true;
+  }
+};
+
+// A wait that ends the same way for every lane of the warp: by one lane's poll, or by all.
+__device__ __forceinline__ bool wait_lane0(uint64_t* bar, uint32_t parity, int lane, volatile int* abort,
+                                           const int* gerr) {
+  int ok = 1;
+  if (lane == 0) ok = wait_bounded(bar, parity, abort, gerr);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, const int* gerr) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, gerr));
+}
+
+// S[128 x 64] = Q K^T, both K-major.
+template <int HD>
+__device__ __forceinline__ void issue_s(uint32_t d, uint32_t sq, uint32_t sk, uint32_t idesc) {
+  const uint64_t dq = sdesc_sw128(sq, 16, 1024), dk = sdesc_sw128(sk, 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk)
+    mma_ss(d, sdesc_add(dq, (kk / 4) * QBOX + (kk % 4) * 32), sdesc_add(dk, (kk / 4) * KBOX + (kk % 4) * 32), idesc,
+           kk > 0 ? 1u : 0u);
+}
+
+// O[128 x HD] (+)= P V: P from TMEM, V seen MN-major.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t tp, uint32_t sv, uint32_t idesc, bool first) {
+  const uint64_t dv = sdesc_sw128(sv, KBOX, 1024);
+#pragma unroll
+  for (int kk = 0; kk < BN / 16; ++kk)
+    mma_ts(d, tp + kk * 8, sdesc_add(dv, kk * 2048), idesc, (first && kk == 0) ? 0u : 1u);
+}
+
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (FP16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return pack_bf16x2(lo, hi);
+}
+template <bool FP16>
+__device__ __forceinline__ float unpack16(uint16_t x) {
+  if (FP16) {
+    const __half_raw r = {x};
+    return __half2float(__half(r));
+  }
+  return __uint_as_float((uint32_t)x << 16);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// P row = exp2(s * sl2 - m), zero in columns whose bit of (lo, hi) is clear (MASK), as 16-bit
+// pairs over the first 32 columns of the row's S buffer; returns the fp32 row sum.
+template <bool FP16, bool MASK>
+__device__ __forceinline__ float p_row(const uint32_t (&sr)[64], uint32_t lo, uint32_t hi, float sl2, float neg_m,
+                                       uint32_t t_s) {
+  const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(neg_m, neg_m);
+  float2 sp[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sp[e] = make_float2(0.f, 0.f);
+  uint32_t pk[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    const float2 x =
+        __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), scale2, shift2);
+    float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+    if (MASK) {
+      const uint32_t w = c < 16 ? lo : hi;
+      p0 = (w >> (2 * c % 32)) & 1u ? p0 : 0.f;
+      p1 = (w >> (2 * c % 32 + 1)) & 1u ? p1 : 0.f;
+    }
+    sp[c % 4].x += p0;
+    sp[c % 4].y += p1;
+    pk[c] = pack16<FP16>(p0, p1);
+  }
+  tmem_st_x32(t_s, pk);
+  return ((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y));
+}
+
+// Clears V rows [keep, 64) of a tile and, with `scan`, the elements of the others that are
+// infinite or NaN, whose rows it notes in bad[2].  Row r of column box x lies at
+// x * KBOX + r * 128 whatever the swizzle, which only permutes 16-byte pieces of the row.
+template <int HD, bool FP16>
+__device__ __forceinline__ void clean_v(uint8_t* v, int keep, bool scan, uint32_t* bad, int tid, int nthreads) {
+  const uint32_t exp_mask = FP16 ? 0x7c00u : 0x7f80u;
+  for (int i = tid; i < BN * (HD / 8); i += nthreads) {
+    const int c = i % (HD / 8), r = i / (HD / 8);   // c: 16-byte piece of the row
+    uint4* at = reinterpret_cast<uint4*>(v + (c / 8) * KBOX + r * 128 + (c % 8) * 16);
+    if (r >= keep) {
+      *at = make_uint4(0, 0, 0, 0);
+    } else if (scan) {
+      uint4 u = *at;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((w[e] & exp_mask) == exp_mask) w[e] &= 0xffff0000u, any = true;
+        if (((w[e] >> 16) & exp_mask) == exp_mask) w[e] &= 0x0000ffffu, any = true;
+      }
+      if (any) {
+        *at = u;
+        atomicOr(&bad[r / 32], 1u << (r % 32));
+      }
+    }
+  }
+}
+
+template <int HD, bool FP16>
+__global__ void __launch_bounds__(NTHREADS, 2)
+    tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkp,
+                const __grid_constant__ CUtensorMap tvp, const __grid_constant__ CUtensorMap tkn,
+                const __grid_constant__ CUtensorMap tvn, const Params p) {
+  using C = Cfg<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* s_full = v_empty + VST;     // [2]
+  uint64_t* p_ready = s_full + 2;       // [2]
+  uint64_t* pv_done = s_full + 4;
+  uint64_t* o_full = s_full + 5;
+  uint64_t* o_free = s_full + 6;
+  uint64_t* noted = s_full + 7;         // drafted rows with inf/NaN are noted
+  uint64_t* drain = s_full + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* run = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);        // sequence, tile, tiles, runs in use
+  uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 32);  // [3][4]: drafted rows with inf/NaN
+  int* s_len = reinterpret_cast<int*>(smem + C::OFF_LEN);
+  int* s_new = s_len + kTreeMaxB;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int U = p.Hkv * p.RT;
+  const int u = (int)blockIdx.x % U, j = (int)blockIdx.x / U;
+  const int kvh = u / p.RT, rt = u % p.RT;
+  const int first_tok = rt * p.tok;                              // the row tile's first drafted token
+  const int tile_toks = min(p.tok, p.M - first_tok);
+  const int n_act = (tile_toks * p.group + 31) / 32;             // softmax warps with rows
+
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) report_error(p.err, (K_TREE << 8) | SITE_ALIGN);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < KST; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_ready[s], n_act);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, n_act);
+    mbar_init(noted, n_act);
+    mbar_init(drain, 1);
+    *abort_flag = (*(volatile int*)p.err != 0) ? 1 : 0;
+    for (int i = 0; i < 12; ++i) bad[i] = 0;
+    fence_mbar_init();
+  }
+  // lengths, clamped to what the tables can hold
+  const int cap = cap_tokens(p);
+  for (int b = threadIdx.x; b < p.B; b += NTHREADS) {
+    const int l = p.len[b], nw = p.new_len ? p.new_len[b] : p.M;
+    const int lc = min(max(l, 0), cap), nc = min(max(nw, 0), p.M);
+    if (lc != l || nc != nw) report_error(p.index_err, (K_TREE << 8) | SITE_INDEX);
+    s_len[b] = lc;
+    s_new[b] = nc;
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(tmem_slot, TM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp == 0) {
+    // this CTA's run: tiles [w0, w1) of the unit's concatenation
+    long long sum = 0;
+    for (int b = lane; b < p.B; b += 32) sum += all_tiles(s_len[b], s_new[b], first_tok);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int runs = (int)min((long long)p.J, max(1LL, sum / kTreeMinRun));
+    long long w0 = 0, w1 = 0;
+    if (j < runs) {
+      w0 = sum * j / runs;
+      w1 = sum * (j + 1) / runs;
+    }
+    // the sequence that holds tile w0
+    int b0 = 0, t0 = 0;
+    long long before = 0;
+    for (int base = 0; base < p.B && w1 > w0; base += 32) {
+      const int b = base + lane;
+      const long long mine = b < p.B ? all_tiles(s_len[b], s_new[b], first_tok) : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + incl > w0);
+      if (past) {
+        const int f = __ffs(past) - 1;
+        b0 = base + f;
+        t0 = (int)(w0 - before - __shfl_sync(0xffffffffu, incl - mine, f));
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      run[0] = b0;
+      run[1] = t0;
+      run[2] = (int)(w1 - w0);
+      run[3] = runs;
+    }
+  }
+  __syncthreads();
+  const int n_tiles = run[2];
+  const bool skip = *abort_flag != 0 || n_tiles == 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Segments seg(s_len, s_new, first_tok, run[0], run[1], n_tiles);
+
+  if (!skip && (warp == WARP_K || warp == WARP_V)) {
+    // ---------------- producers: Q and K, or V ----------------
+    const bool is_k = warp == WARP_K;
+    const CUtensorMap* mp = is_k ? &tkp : &tvp;
+    const CUtensorMap* mn = is_k ? &tkn : &tvn;
+    uint64_t* full = is_k ? k_full : v_full;
+    uint64_t* empty = is_k ? k_empty : v_empty;
+    uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+    constexpr int NST = KST;
+    static_assert(KST == VST, "one ring depth");
+    const int box_keys = min(1 << p.page_shift, BN);
+    const int new_box = min(p.M, BN);
+    if (lane == 0) {
+      if (is_k) prefetch_tmap(&tq);
+      prefetch_tmap(mp);
+      prefetch_tmap(mn);
+    }
+    bool ok = true;
+    int i = 0, n_seg = 0;
+    while (ok && seg.next()) {
+      const int b = seg.b, len = s_len[b], ct = cache_tiles(len);
+      const int used = (int)(((long long)len + (1 << p.page_shift) - 1) >> p.page_shift);
+      if (is_k) {
+        // Q rows (token, head of the group) of the row tile
+        if (n_seg > 0) ok = wait_lane0(q_empty, (n_seg - 1) & 1, lane, abort_flag, p.err);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, C::NB * 128 * p.group * min(p.tok, p.M));
+          for (int x = 0; x < C::NB; ++x)
+            tma_load_3d(smem + x * QBOX, &tq, x * 64, kvh * p.group, b * p.M + first_tok, q_full);
+        }
+        ++n_seg;
+      }
+      // page numbers, 32 at a time, the next 32 on the way
+      int base = ((long long)seg.t0 * BN) >> p.page_shift;
+      const int* row = p.table + (size_t)b * p.width;
+      int ids = base + lane < used ? row[base + lane] : -1;
+      int ids_next = base + 32 + lane < used ? row[base + 32 + lane] : -1;
+      for (int t = seg.t0; t < seg.t0 + seg.n; ++t, ++i) {
+        const int slot = i % NST;
+        if (i >= NST) ok = wait_lane0(&empty[slot], ((i / NST) - 1) & 1, lane, abort_flag, p.err);
+        if (!ok) break;
+        uint8_t* dst = ring + slot * C::KTILE;
+        if (t < ct) {
+          const int key0 = t * BN;
+          const int boxes = (min(BN, len - key0) + box_keys - 1) / box_keys;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * C::NB * box_keys * 128);
+          for (int x = 0; x < boxes; ++x) {
+            const int key = key0 + x * box_keys;
+            const int pg = key >> p.page_shift;
+            if (pg - base >= 32) {
+              base += 32;
+              ids = ids_next;
+              ids_next = base + 32 + lane < used ? row[base + 32 + lane] : -1;
+            }
+            int id = __shfl_sync(0xffffffffu, ids, pg - base);
+            if (id < 0 || id >= p.n_pages) {   // recorded; the box reads as zeros
+              if (lane == 0) report_error(p.index_err, (K_TREE << 8) | SITE_INDEX);
+              id = p.n_pages;
+            }
+            if (lane == 0) {
+              const int r = (id << p.page_shift) + (id < p.n_pages ? key & ((1 << p.page_shift) - 1) : 0);
+              for (int y = 0; y < C::NB; ++y)
+                tma_load_3d(dst + y * KBOX + x * box_keys * 128, mp, y * 64, kvh, r, &full[slot]);
+            }
+          }
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(&full[slot], C::NB * new_box * 128);
+          for (int y = 0; y < C::NB; ++y)
+            tma_load_3d(dst + y * KBOX, mn, y * 64, kvh, b * p.M + (t - ct) * BN, &full[slot]);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      report_error(p.err, (K_TREE << 8) | SITE_LOAD);
+      *abort_flag = 1;
+    }
+    if (lane == 0) {
+      bool dok = true;
+      if (is_k && n_seg > 0) dok &= wait_drain(q_full, (n_seg - 1) & 1);
+      for (int s = (i > NST ? i - NST : 0); s < i; ++s) dok &= wait_drain(&full[s % NST], (s / NST) & 1);
+      if (!dok) report_error(p.err, (K_TREE << 8) | SITE_DRAIN);
+    }
+    __syncwarp();
+  } else if (!skip && warp == WARP_MMA) {
+    if (lane == 0) {
+      // ---------------- MMA issuer: S(i) | P(i-1) V(i-1) ----------------
+      const uint32_t fmt = FP16 ? ~((1u << 7) | (1u << 10)) : ~0u;   // A and B formats: 0 = f16, 1 = bf16
+      const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false) & fmt;
+      const uint32_t id_pv = idesc_bf16_f32(BM, HD, false, true) & fmt;
+      const uint32_t sq = smem_u32(smem), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
+      bool ok = true;
+      int ns = 0, np = 0;             // segments whose S, whose first PV was issued
+      int s_left = 0, pv_left = 0;    // tiles left in the segment of S and of PV
+      Segments sp(s_len, s_new, first_tok, run[0], run[1], n_tiles);
+      for (int i = 0; i <= n_tiles && ok; ++i) {
+        if (i < n_tiles) {
+          if (s_left == 0) {
+            seg.next();
+            s_left = seg.n;
+            ok = wait_spin(q_full, ns & 1, abort_flag, p.err);
+            ++ns;
+          }
+          if (ok) ok = wait_spin(&k_full[i % KST], (i / KST) & 1, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s<HD>(tmem + (uint32_t)BN * (i & 1), sq, sk + (i % KST) * C::KTILE, id_s);
+          mma_commit(&s_full[i & 1]);
+          mma_commit(&k_empty[i % KST]);
+          if (--s_left == 0) mma_commit(q_empty);
+        }
+        if (i > 0) {
+          const int t = i - 1;
+          bool first = false;
+          if (pv_left == 0) {
+            sp.next();
+            pv_left = sp.n;
+            first = true;
+            if (np > 0) ok = wait_spin(o_free, (np - 1) & 1, abort_flag, p.err);   // O of the last segment read
+            ++np;
+          }
+          if (ok) ok = wait_spin(&p_ready[t & 1], (t >> 1) & 1, abort_flag, p.err);
+          if (ok) ok = wait_spin(&v_full[t % VST], (t / VST) & 1, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(tmem + TM_O, tmem + (uint32_t)BN * (t & 1), sv + (t % VST) * C::KTILE, id_pv, first);
+          mma_commit(pv_done);
+          mma_commit(&v_empty[t % VST]);
+          if (--pv_left == 0) mma_commit(o_full);
+        }
+      }
+      if (!ok) {
+        report_error(p.err, (K_TREE << 8) | SITE_MMA);
+        *abort_flag = 1;
+      }
+      mma_commit(drain);
+      if (!wait_drain(drain, 0)) report_error(p.err, (K_TREE << 8) | SITE_DRAIN);
+    }
+    __syncwarp();
+  } else if (!skip && warp < n_act) {
+    // ---------------- softmax: thread = query row ----------------
+    const int r = warp * 32 + lane;
+    const int m = first_tok + r / p.group;                  // drafted token of the row
+    const int h = kvh * p.group + r % p.group;
+    const bool in_tile = r < tile_toks * p.group;
+    const uint32_t lane_addr = tmem + ((uint32_t)(warp * 32) << 16);
+    const float sl2 = p.sl2;
+    bool ok = true;
+    int i = 0, n_seg = 0, n_draft = 0;
+    while (ok && seg.next()) {
+      const int b = seg.b, len = s_len[b], nw = s_new[b], ct = cache_tiles(len);
+      const bool row_ok = in_tile && m < nw;
+      uint32_t* bad_rows = bad + 4 * (n_draft % 3);        // of this sequence's drafted tiles
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int t = seg.t0; t < seg.t0 + seg.n && ok; ++t, ++i) {
+        const int buf = i & 1;
+        // keys of the tile, and which of them the row sees
+        const bool draft = t >= ct;
+        const int keep = draft ? min(BN, nw - (t - ct) * BN) : min(BN, len - t * BN);
+        const bool edge = draft || keep < BN;
+        uint32_t lo = 0xffffffffu, hi = 0xffffffffu;
+        if (edge) {
+          unsigned long long vis = keep >= 64 ? ~0ull : (1ull << keep) - 1ull;
+          if (draft) {
+            const int d = t - ct;
+            if (!row_ok) {
+              vis = 0;
+            } else if (p.mask) {
+              vis &= p.mask[((size_t)b * p.M + m) * p.words + d];
+            } else {
+              const int last = m - d * BN;                 // j <= m
+              vis &= last >= 63 ? ~0ull : last < 0 ? 0ull : (2ull << last) - 1ull;
+            }
+          }
+          lo = (uint32_t)vis;
+          hi = (uint32_t)(vis >> 32);
+          ok = wait_warp(&v_full[i % VST], (i / VST) & 1, abort_flag, p.err);
+          if (!ok) break;
+          clean_v<HD, FP16>(smem + C::OFF_V + (i % VST) * C::KTILE, keep, draft, bad_rows + 2 * (draft ? t - ct : 0),
+                            threadIdx.x, n_act * 32);
+          fence_proxy_async_smem();
+        }
+        ok = wait_warp(&s_full[buf], (i >> 1) & 1, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t_s = lane_addr + (uint32_t)BN * buf;
+        uint32_t s0[64];
+        tmem_ld_x64(t_s, s0);
+        float mxp[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mxp[e] = -INFINITY;
+        if (!edge) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            mxp[c % 8] = max3(mxp[c % 8], __uint_as_float(s0[2 * c]), __uint_as_float(s0[2 * c + 1]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint32_t w = c < 16 ? lo : hi;
+            mxp[c % 8] = max3(mxp[c % 8], (w >> (2 * c % 32)) & 1u ? __uint_as_float(s0[2 * c]) : -INFINITY,
+                              (w >> (2 * c % 32 + 1)) & 1u ? __uint_as_float(s0[2 * c + 1]) : -INFINITY);
+          }
+        }
+        const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
+                               fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
+        // the running max moves only when it grows by more than 2^8 (P then stays below 2^8,
+        // inside fp16's range too); a row that has seen no key keeps -inf and its P stays 0
+        const float m_new = fmaxf(m_run, mx * sl2);
+        const bool need = (m_new - m_run) > 8.0f;
+        const bool rescale = __any_sync(0xffffffffu, need);
+        const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
+        if (need) m_run = m_new;
+        l_run *= alpha;
+        l_run += edge ? p_row<FP16, true>(s0, lo, hi, sl2, -m_run, t_s) : p_row<FP16, false>(s0, lo, hi, sl2, -m_run, t_s);
+        if (rescale && t > seg.t0) {
+          // O was last written by the previous tile's product: wait for it, then scale the row
+          ok = wait_warp(pv_done, (i - 1) & 1, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t rr[32];
+            tmem_ld_x32(lane_addr + TM_O + c, rr);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+            tmem_st_x32(lane_addr + TM_O + c, rr);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready[buf]);
+      }
+      if (ok) ok = wait_warp(o_full, n_seg & 1, abort_flag, p.err);
+      if (!ok) break;
+      tc_fence_after();
+      const bool has_draft = seg.t0 + seg.n > ct;
+      uint32_t fix[4] = {0, 0, 0, 0};      // drafted rows with inf/NaN that this row sees
+      if (has_draft) {
+        // every warp has noted its rows; the notes of the sequence after the next start from
+        // zero (all warps have read what is cleared here, none writes it before the next wait)
+        if (lane == 0) mbar_arrive(noted);
+        ok = wait_warp(noted, n_draft & 1, abort_flag, p.err);
+        if (!ok) break;
+        if (threadIdx.x < 4) bad[4 * ((n_draft + 2) % 3) + threadIdx.x] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          fix[e] = row_ok ? bad_rows[e] : 0u;
+          if (fix[e] == 0) continue;
+          uint32_t see;
+          if (p.mask) {
+            see = e / 2 < p.words ? (uint32_t)(p.mask[((size_t)b * p.M + m) * p.words + e / 2] >> (32 * (e % 2))) : 0u;
+          } else {
+            const int last = m - e * 32;
+            see = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
+          }
+          fix[e] &= see;
+        }
+        ++n_draft;
+      }
+      const bool whole = seg.t0 == 0 && seg.n == seg.total;
+      const size_t part = ((size_t)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0)) * p.slot_rows + r;
+      const size_t orow = ((size_t)b * p.M + m) * p.H + h;
+      const bool st_ok =
+          row_ok && (whole ? in_bounds(orow, 1, (size_t)p.B * p.M * p.H, p.err, (K_TREE << 8) | SITE_STORE)
+                           : in_bounds(part, 1, (size_t)gridDim.x * 2 * p.slot_rows, p.err, (K_TREE << 8) | SITE_STORE));
+      const float inv = l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f;   // a row that sees nothing: 0
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t rr[32];
+        __syncwarp();
+        tmem_ld_x32(lane_addr + TM_O + c, rr);
+        for (int e = 0; e < 4; ++e) {
+          for (uint32_t left = fix[e]; left; left &= left - 1) {
+            const int key = e * 32 + __ffs(left) - 1;
+            const uint16_t* v = static_cast<const uint16_t*>(p.v_new) + (((size_t)b * p.M + key) * p.Hkv + kvh) * HD + c;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float f = unpack16<FP16>(v[x]);
+              if (!isfinite(f)) rr[x] = __float_as_uint(__uint_as_float(rr[x]) + f);
+            }
+          }
+        }
+        if (st_ok && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * HD + c);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              w[y] = pack16<FP16>(__uint_as_float(rr[8 * x + 2 * y]) * inv, __uint_as_float(rr[8 * x + 2 * y + 1]) * inv);
+            dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (st_ok) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + part * HD + c);
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            dst[x] = make_float4(__uint_as_float(rr[4 * x]), __uint_as_float(rr[4 * x + 1]),
+                                 __uint_as_float(rr[4 * x + 2]), __uint_as_float(rr[4 * x + 3]));
+        }
+      }
+      if (st_ok) {
+        if (whole) {
+          p.lse[((size_t)b * p.H + h) * p.M + m] =
+              l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+        } else {
+          p.part_ml[part * 2] = m_run;
+          p.part_ml[part * 2 + 1] = l_run;
+        }
+      }
+      if (kvh == 0 && threadIdx.x == 0) {
+        if (seg.t0 == 0) p.meta[(b * p.RT + rt) * 2] = j;
+        if (seg.t0 + seg.n == seg.total) p.meta[(b * p.RT + rt) * 2 + 1] = j;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      ++n_seg;
+    }
+    if (!ok) {
+      report_error(p.err, (K_TREE << 8) | SITE_SOFTMAX);
+      *abort_flag = 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TM_COLS);
+  }
+}
+
+// o = sum_s 2^(m_s - mx) o_s / sum_s 2^(m_s - mx) l_s over the runs s of the row's sequence;
+// lse = ln2 * (mx + log2 L).  One block per (b, m, h) row: every warp reads all (max, sum)
+// pairs, then takes every fourth run's output.  Rows of a sequence that lay in one run were
+// written by the run.
+constexpr int CW = 4;
+template <int HD, bool FP16>
+__global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_constant__ Params p) {
+  constexpr int PER = HD / 32;
+  __shared__ float part[CW][HD];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int h = (int)(blockIdx.x % p.H);
+  const int m = (int)((blockIdx.x / p.H) % p.M);
+  const int b = (int)(blockIdx.x / ((unsigned)p.H * p.M));
+  // launched as a programmatic dependent of the attention kernel: wait for that whole grid
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int nw = p.new_len ? min(p.new_len[b], p.M) : p.M;
+  if (m >= nw || *(volatile int*)p.err != 0) return;
+  const int rt = m / p.tok, kvh = h / p.group;
+  const int first = max(p.meta[(b * p.RT + rt) * 2], 0), last = min(p.meta[(b * p.RT + rt) * 2 + 1], p.J - 1);
+  if (first >= last) return;
+  const int U = p.Hkv * p.RT, u = kvh * p.RT + rt;
+  const int r = (m - rt * p.tok) * p.group + h % p.group;
+  // run s: slot 1 of CTA (u, first), slot 0 of the later ones
+  auto row_of = [&](int s) { return (((size_t)s * U + u) * 2 + (s == first ? 1 : 0)) * p.slot_rows + r; };
+  float mx = -INFINITY;
+  for (int s = first + lane; s <= last; s += 32) mx = fmaxf(mx, p.part_ml[row_of(s) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float L = 0.f;
+  float acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  if (mx != -INFINITY) {
+    for (int s = first + lane; s <= last; s += 32)
+      L += exp2f(p.part_ml[row_of(s) * 2] - mx) * p.part_ml[row_of(s) * 2 + 1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll 4
+    for (int s = first + warp; s <= last; s += CW) {
+      const size_t row = row_of(s);
+      const float w = exp2f(p.part_ml[row * 2] - mx);
+      alignas(16) float v[PER];
+      if constexpr (PER == 4)
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p.part_o + row * HD + lane * PER);
+      else
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p.part_o + row * HD + lane * PER);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) part[warp][lane * PER + e] = acc[e];
+  __syncthreads();
+  const float inv = mx == -INFINITY ? 0.f : 1.0f / L;
+  const size_t orow = ((size_t)b * p.M + m) * p.H + h;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + orow * HD);
+  for (int c = threadIdx.x; c < HD / 2; c += CW * 32) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < CW; ++w) {
+      x += part[w][2 * c];
+      y += part[w][2 * c + 1];
+    }
+    dst[c] = pack16<FP16>(x * inv, y * inv);
+  }
+  if (threadIdx.x == 0)
+    p.lse[((size_t)b * p.H + h) * p.M + m] = mx == -INFINITY ? -INFINITY : (mx + log2f(L)) * 0.69314718055994531f;
+}
+
+template <int HD, bool FP16>
+cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
+  using C = Cfg<HD>;
+  // the shared-memory limit is a per-device function attribute: set it once per device
+  static std::atomic<uint64_t> done_mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
+  if (!bit || !(done_mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(tree_kernel<HD, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    done_mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const unsigned grid = (unsigned)(p.Hkv * p.RT * p.J);
+  tree_kernel<HD, FP16><<<grid, NTHREADS, C::SMEM, st>>>(t.q, t.k_pages, t.v_pages, t.k_new, t.v_new, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.J == 1) return e;   // one run: every sequence was written whole
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p.B * p.M * p.H));
+  cfg.blockDim = dim3(CW * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, FP16>, p);
+}
+
+}  // namespace tree
+
+// Row tiles and runs.  A unit's J CTAs should fill whole waves of two CTAs an SM: the J up to
+// two waves' worth with the least ceil(U * J / slots) / J (the time of a unit's share times
+// the waves it takes), the smaller one on a tie, since each run more costs partials.
+TreePlan tree_plan(int M, int H, int Hkv) {
+  TreePlan t;
+  t.group = H / Hkv;
+  t.tok = tree::BM / t.group;
+  t.RT = (M + t.tok - 1) / t.tok;
+  const long long U = (long long)Hkv * t.RT;
+  t.slot_rows = (t.tok < M ? t.tok : M) * t.group;
+  t.J = 1;
+  double best = 1e30;
+  for (int J = 1; J == 1 || U * J <= 2 * kTreeSlots; ++J) {
+    const double cost = (double)((U * J + kTreeSlots - 1) / kTreeSlots) / J;
+    if (cost < best - 1e-9) {
+      best = cost;
+      t.J = J;
+    }
+  }
+  return t;
+}
+
+cudaError_t launch_tree_decode(const TreeMaps& maps, const TreeArgs& a, const TreePlan& t, cudaStream_t st) {
+  tree::Params p{};
+  p.o = a.o, p.lse = a.lse, p.part_o = a.part_o, p.part_ml = a.part_ml, p.meta = a.meta;
+  p.len = a.cache_len, p.new_len = a.new_len, p.table = a.page_table, p.mask = a.mask, p.v_new = a.v_new;
+  p.B = a.B, p.M = a.M, p.H = a.H, p.Hkv = a.Hkv, p.group = t.group, p.RT = t.RT, p.tok = t.tok, p.J = t.J;
+  p.slot_rows = t.slot_rows;
+  p.page_shift = a.page_shift, p.n_pages = a.n_pages, p.width = a.width, p.words = (a.M + 63) / 64;
+  p.sl2 = (float)(1.4426950408889634 / std::sqrt((double)a.D));
+  p.err = a.err, p.index_err = a.index_err;
+  const bool fp16 = a.dtype == S2ATTN_FP16;
+  if (a.D == 128) return fp16 ? tree::launch<128, true>(maps, p, st) : tree::launch<128, false>(maps, p, st);
+  return fp16 ? tree::launch<64, true>(maps, p, st) : tree::launch<64, false>(maps, p, st);
+}
+
+}  // namespace s2

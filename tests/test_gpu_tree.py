@@ -1,0 +1,263 @@
+"""s2attn_tree_mask and s2attn_tree_decode against 64-bit attention over the gathered cache.
+
+The pools' unused rows and pages hold NaN, so that a key that must not be seen shows.  The
+bounds are derived in serving_utils.attend.
+"""
+import random
+
+import pytest
+import torch
+
+import shifted_sparse_attention_s2attn_b200 as s2
+from serving_utils import (attend, check_close, make_cache, no_device_error, random_parents, tree_see, words_of)
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    s2.clear_device_error()
+
+
+@pytest.mark.parametrize("B,M", [(1, 1), (3, 2), (2, 13), (1, 63), (2, 64), (1, 65), (2, 128)])
+def test_tree_mask(B, M):
+    rng = random.Random(M)
+    trees = random_parents(B, M, rng)
+    trees[0] = list(range(-1, M - 1))      # a chain, the deepest tree
+    see, depth = tree_see(trees)
+    mask = torch.full((B, M, (M + 63) // 64), -1, dtype=torch.int64, device="cuda")
+    dep = torch.full((B, M), -1, dtype=torch.int32, device="cuda")
+    par = torch.tensor(trees, dtype=torch.int32, device="cuda")
+    s2.s2attn_tree_mask(par, mask, dep)
+    no_device_error()
+    assert torch.equal(mask.cpu(), words_of(see)) and torch.equal(dep.cpu(), depth)
+    mask.zero_()
+    s2.s2attn_tree_mask(par, mask)
+    no_device_error()
+    assert torch.equal(mask.cpu(), words_of(see))
+
+
+def test_tree_mask_records_bad_parents():
+    par = torch.tensor([[-1, 0, 2, 1], [-1, 0, 1, 2], [-2, 0, 0, 9]], dtype=torch.int32, device="cuda")
+    mask = torch.zeros(3, 4, 1, dtype=torch.int64, device="cuda")
+    s2.s2attn_tree_mask(par, mask)
+    torch.cuda.synchronize()
+    assert s2.get_device_error() == (-6, 0x640)
+    s2.clear_device_error()
+    assert mask[1, :, 0].tolist() == [1, 3, 7, 15]
+    assert mask[0, :, 0].tolist() == [1, 3, 4, 11] and mask[2, :, 0].tolist() == [1, 3, 5, 8]
+
+
+def _case(lens, M, H, Hkv, D, page, dt, mask, new=None, seed=0, fill=float("nan"), q_scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    B = len(lens)
+    rnd = lambda *s: torch.randn(s, generator=g).to(dt)
+    kp, vp, table, n = make_cache(lens, 0, page, Hkv, D, dt, seed + 1, fill=fill)
+    c = dict(q=(rnd(B, M, H, D) * q_scale), k_new=rnd(B, M, Hkv, D), v_new=rnd(B, M, Hkv, D), k_pages=kp, v_pages=vp,
+             page_table=table, cache_len=n)
+    rng = random.Random(seed)
+    if mask == "chain":
+        see, words = torch.ones(M, M, dtype=torch.bool).tril().expand(B, M, M), None
+    elif mask == "tree":
+        see, _ = tree_see(random_parents(B, M, rng))
+        words = words_of(see)
+    else:      # any bits: later tokens seen, own token not, rows that see nothing
+        see = torch.rand(B, M, M, generator=g) < 0.4
+        see[:, ::3] = False
+        words = words_of(see)
+    new = [M] * B if new is None else new
+    for b, m in enumerate(new):     # rows that do not exist hold NaN too
+        for t in ("q", "k_new", "v_new"):
+            c[t][b, m:] = float("nan")
+    return c, see, words, new
+
+
+def _run(c, words, new, ragged, o_fill=7.0):
+    d = {n: t.cuda() for n, t in c.items()}
+    B, M, H, D = c["q"].shape
+    o = torch.full_like(d["q"], o_fill)
+    lse = torch.full((B, H, M), o_fill, dtype=torch.float32, device="cuda")
+    ws = torch.empty(s2.s2attn_tree_decode_workspace_bytes(B, M, H, c["k_new"].shape[2], D), dtype=torch.uint8,
+                     device="cuda").fill_(0xff)
+    s2.s2attn_tree_decode(d["q"], d["k_new"], d["v_new"], d["k_pages"], d["v_pages"], d["page_table"], d["cache_len"],
+                          o, lse, ws, tree_mask=None if words is None else words.cuda(),
+                          new_len=torch.tensor(new, dtype=torch.int32, device="cuda") if ragged else None)
+    return o.cpu(), lse.cpu()
+
+
+def _check(c, see, words, new, ragged=True):
+    o, lse = _run(c, words, new, ragged)
+    no_device_error()
+    wo, wl, bo, bl = attend(c["q"], c["k_new"], c["v_new"], c["k_pages"], c["v_pages"], c["page_table"], c["cache_len"],
+                            see, new)
+    for b, m in enumerate(new):
+        assert (o[b, m:] == 7).all() and (lse[b, :, m:] == 7).all(), "rows behind the last drafted token changed"
+        check_close(o[b, :m], wo[b, :m], bo[b, :m], f"o of sequence {b}")
+        check_close(lse[b, :, :m], wl[b, :, :m], bl[b, :, :m], f"lse of sequence {b}")
+    return o, lse
+
+
+@pytest.mark.parametrize("lens,M,H,Hkv,D,page,dt", [
+    ([0], 1, 1, 1, 128, 16, BF),                       # nothing cached, one token
+    ([1], 1, 1, 1, 64, 16, FP),
+    ([63, 64, 65], 1, 4, 4, 128, 64, BF),              # tile borders
+    ([15, 16, 17, 0, 130], 3, 8, 2, 64, 16, FP),       # pages that end inside a tile
+    ([300, 7], 13, 8, 1, 128, 32, BF),
+    ([200], 64, 8, 8, 128, 128, FP),
+    ([129, 31], 65, 2, 1, 64, 256, BF),                # two drafted tiles
+    ([70], 128, 3, 3, 128, 16, BF),
+    ([90, 1], 30, 10, 2, 128, 16, FP),                 # five heads a key head: row tiles of 25 tokens
+    ([100], 40, 8, 1, 64, 64, BF),                     # three row tiles
+    ([40], 2, 128, 1, 128, 16, BF),                    # one token a row tile
+    ([33], 5, 7, 1, 64, 16, FP),
+    ([2900], 2, 2, 1, 128, 64, BF),                    # one sequence over many runs
+    ([1, 700, 0, 64, 0, 200, 33, 5], 4, 2, 1, 64, 16, FP),
+])
+@pytest.mark.parametrize("mask", ["chain", "tree", "any"])
+def test_attention(lens, M, H, Hkv, D, page, dt, mask):
+    _check(*_case(lens, M, H, Hkv, D, page, dt, mask), ragged=False)
+
+
+@pytest.mark.parametrize("mask", ["chain", "tree", "any"])
+def test_ragged_batches(mask):
+    rng = random.Random(5)
+    for seed, B, M, H, Hkv, D in [(1, 9, 20, 4, 2, 64), (2, 3, 70, 8, 1, 64), (3, 40, 3, 2, 2, 128)]:
+        lens = [rng.choice([0, 1, 64, rng.randint(0, 400)]) for _ in range(B)]
+        new = [rng.choice([0, 1, M, rng.randint(0, M)]) for _ in range(B)]
+        new[0] = 0
+        _check(*_case(lens, M, H, Hkv, D, 16, BF, mask, new=new, seed=seed))
+
+
+def test_nothing_to_do():
+    c, see, words, new = _case([40, 0], 3, 2, 1, 64, 16, BF, "chain", new=[0, 0])
+    _check(c, see, words, new)
+
+
+def test_large_scores():
+    """Scores up to several hundred: the running maximum moves in most tiles."""
+    _check(*_case([500, 130], 4, 4, 2, 128, 16, BF, "tree", q_scale=30.0), ragged=False)
+
+
+def test_masked_rows_that_hold_infinities_reach_nobody_else():
+    """Drafted rows with inf and NaN reach exactly the tokens whose mask shows them."""
+    for H, M, mask in [(2, 6, "tree"), (8, 70, "any"), (1, 5, "chain")]:
+        c, see, words, new = _case([70, 0], M, H, 1, 64, 16, FP, mask, seed=4)
+        bad = M - 2
+        c["v_new"][:, bad, :, 3] = float("inf")
+        c["v_new"][:, bad, :, 40] = float("nan")
+        o, lse = _run(c, words, new, False)
+        no_device_error()
+        clean = {n: t.clone() for n, t in c.items()}
+        clean["v_new"][:, bad, :, 3] = clean["v_new"][:, bad, :, 40] = 0.0
+        wo, wl, bo, bl = attend(clean["q"], clean["k_new"], clean["v_new"], clean["k_pages"], clean["v_pages"],
+                                clean["page_table"], clean["cache_len"], see, new)
+        hit = see[:, :, bad]
+        wo[..., 3] = torch.where(hit[:, :, None], float("inf"), wo[..., 3])
+        wo[..., 40] = torch.where(hit[:, :, None], float("nan"), wo[..., 40])
+        check_close(o, wo, bo, "o")
+        check_close(lse, wl, bl, "lse")
+        # a key of NaN makes the scores of those who see it NaN, of nobody else
+        c["v_new"][:, bad] = 1.0
+        c["k_new"][:, bad] = float("nan")
+        o, lse = _run(c, words, new, False)
+        no_device_error()
+        assert torch.equal(o.isnan().all(-1).all(-1), hit) and torch.equal(o.isnan().any(-1).any(-1), hit)
+        assert torch.equal(lse.isnan().all(1), hit)
+
+
+def test_bad_pages_and_lengths_are_recorded_and_stay_in_their_sequence():
+    c, see, words, new = _case([100, 200, 150], 3, 4, 2, 64, 16, BF, "chain")
+    wo, wl, bo, bl = attend(*[c[n] for n in ("q", "k_new", "v_new", "k_pages", "v_pages", "page_table", "cache_len")],
+                            see, new)
+    for what, value in [("page", -1), ("page", 10 ** 9), ("page", c["k_pages"].shape[0]), ("len", -5), ("len", 10 ** 9)]:
+        x = {n: t.clone() for n, t in c.items()}
+        if what == "page":
+            x["page_table"][1, 3] = value
+        else:
+            x["cache_len"][1] = value
+            if value > 0:      # the clamped length meets the table's unused entries
+                x["page_table"][1][x["page_table"][1] < 0] = 0
+        o, lse = _run(x, words, new, False)
+        torch.cuda.synchronize()
+        assert s2.get_device_error() == (-6, 0x640), (what, value)
+        s2.clear_device_error()
+        for b in (0, 2):
+            check_close(o[b], wo[b], bo[b], f"o of sequence {b} beside {what} {value}")
+            check_close(lse[b], wl[b], bl[b], f"lse of sequence {b}")
+    # drafted counts outside 0..M
+    for value in (-1, 4):
+        o, lse = _run(c, words, [3, value, 3], True)
+        torch.cuda.synchronize()
+        assert s2.get_device_error() == (-6, 0x640)
+        s2.clear_device_error()
+        check_close(o[2], wo[2], bo[2], "o of sequence 2")
+    no_device_error()
+
+
+def test_repeats_are_bitwise_equal():
+    c, see, words, new = _case([900, 64, 333], 9, 8, 2, 128, 16, BF, "tree")
+    a = _run(c, words, new, False)
+    for _ in range(3):
+        b = _run(c, words, new, False)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_captured_call_follows_the_lengths():
+    """A captured call on a stream of its own, replayed after the cache has grown, while another call
+    with a workspace of its own runs on a second stream."""
+    page, Hkv, D, H, M, B = 16, 2, 64, 4, 2, 3
+    lens = [10, 60, 0]
+    c, see, words, new = _case(lens, M, H, Hkv, D, page, BF, "chain")
+    kp, vp, table, n = make_cache(lens, 200, page, Hkv, D, BF, 9, fill=0.25)
+    c.update(k_pages=kp, v_pages=vp, page_table=table, cache_len=n)
+    d = {x: t.cuda() for x, t in c.items()}
+    o, o2 = torch.empty_like(d["q"]), torch.empty_like(d["q"])
+    lse, lse2 = (torch.empty(B, H, M, device="cuda") for _ in range(2))
+    ws, ws2 = (torch.empty(s2.s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D), dtype=torch.uint8, device="cuda")
+               for _ in range(2))
+    names = ("q", "k_new", "v_new", "k_pages", "v_pages", "page_table", "cache_len")
+    args = [d[x] for x in names]
+    st, st2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        s2.s2attn_tree_decode(*args, o, lse, ws)
+    for grown in ([10, 60, 0], [11, 62, 130], [200, 190, 64]):
+        d["cache_len"].copy_(torch.tensor(grown, dtype=torch.int32))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st2):
+            s2.s2attn_tree_decode(*args, o2, lse2, ws2)
+        with torch.cuda.stream(st):
+            g.replay()
+        no_device_error()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        wo, wl, bo, bl = attend(*[c[x] for x in names[:-1]], torch.tensor(grown), see, new)
+        check_close(o, wo, bo, "o")
+        check_close(lse, wl, bl, "lse")
+
+
+def test_agrees_with_the_contiguous_decoding_step():
+    """The same sequence as a contiguous cache through s2attn_decode: both within their bounds, so
+    within the sum of two output roundings and two P roundings of each other."""
+    N, M, H, D, page = 1000, 4, 4, 128, 64
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(1, n, H, D, generator=g).bfloat16().cuda() for n in (M, N, N))
+    o, lse = torch.empty_like(q), torch.empty(1, H, M, device="cuda")
+    ws = torch.empty(s2.s2attn_decode_workspace_bytes(1, M, N, H, D), dtype=torch.uint8, device="cuda")
+    s2.s2attn_decode(q, k, v, o, lse, ws)
+    n = N - M
+    pages = -(-n // page)
+    kp, vp = (torch.zeros(pages * page, H, D, dtype=BF, device="cuda") for _ in range(2))
+    kp[:n], vp[:n] = k[0, :n], v[0, :n]
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    ws2 = torch.empty(s2.s2attn_tree_decode_workspace_bytes(1, M, H, H, D), dtype=torch.uint8, device="cuda")
+    s2.s2attn_tree_decode(q, k[:, n:].contiguous(), v[:, n:].contiguous(), kp.view(pages, page, H, D),
+                          vp.view(pages, page, H, D), torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                          torch.tensor([n], dtype=torch.int32, device="cuda"), o2, lse2, ws2)
+    no_device_error()
+    # sum p|v| <= max over keys of |v| < 5 times the sum of p; measured outputs are far smaller
+    assert (o.float() - o2.float()).abs().max() <= 2.0 ** -8 * 2 * (o.float().abs().max() + 1)
+    assert (lse - lse2).abs().max() <= 1e-4
