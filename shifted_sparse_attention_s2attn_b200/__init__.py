@@ -6,6 +6,7 @@ the current CUDA stream are passed through, and a non-zero status raises
 S2AttnError.  All arithmetic runs in the CUDA library libs2attn.so; if that library
 is missing, every call raises -- there is no fallback.
 """
+import array
 import ctypes
 import os
 
@@ -150,9 +151,15 @@ def _attn_args(dtype, shape, **tensors):
     _on_cuda(**tensors)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def s2attn_fwd(q, k, v, o, lse, G, shift_heads, stream=None):
@@ -396,45 +403,53 @@ def lora_proj_bwd(x, w, lora_a, lora_b, dy, dx, d_lora_a, d_lora_b, parts, scali
 
 
 # The calls below launch on the device of their tensors, which must be one, whatever the current
-# device is; without a `stream` they take that device's current stream.
+# device is; without a `stream` they take that device's current stream.  They are made once or
+# more per layer and token, so their checks are kept to a few attribute reads a tensor.
 
-def _one_device(**tensors):
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must be on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} must be on {dev} like the other tensors")
-    return dev
+def _fit(t, name, shape, dtype, dev):
+    """A contiguous tensor of this shape and dtype on device `dev` (an index, -1 for the host)."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        where = f"cuda:{dev}" if dev >= 0 else "the host"
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {where} "
+                         "like the other tensors")
 
 
 def _call_on(dev, fn, stream, *args):
+    """Calls the C entry point `fn` with device `dev` current; the stream is its last argument."""
     torch = _torch()
-    if torch.cuda.current_device() == dev.index:
-        rc = getattr(capi(), fn)(*args, _stream(stream))
+    if dev < 0:
+        raise ValueError(f"{fn}: the tensors must be on a CUDA device")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream if isinstance(stream, int) else stream.cuda_stream
+    call = getattr(_lib or capi(), fn)
+    if torch._C._cuda_getDevice() == dev:
+        rc = call(*args, raw)
     else:
         with torch.cuda.device(dev):
-            rc = getattr(capi(), fn)(*args, _stream(stream))
-    _check(fn, rc)
+            rc = call(*args, raw)
+    if rc != 0:
+        raise S2AttnError(fn, rc)
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _dtype_code(t, name, f32):
     torch = _torch()
-    codes = {torch.bfloat16: 0, torch.float16: 1}
-    if f32:
-        codes[torch.float32] = 2
-    if t.dtype not in codes:
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype, 3)
+    if code > (2 if f32 else 1):
         raise ValueError(f"{name} must be bf16{', fp16 or fp32' if f32 else ' or fp16'}")
-    return codes[t.dtype]
+    return code
 
 
-def _shaped(t, name, shape, dtype):
-    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+def _scratch(t, dev):
+    """Address and bytes of a workspace."""
+    if t is None or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the others")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -454,36 +469,44 @@ def rope_inv_freq(R, base=10000.0, scaling="none", factor=1.0, original_len=4096
     return out, af.value
 
 
-def _norm_rope_args(pairs, inv_freq, wq, wk, norm, positions, pos0):
-    """Checks the sides of a call; pairs: [(name, tensor, same-shaped tensors...)] for q and k."""
+def _norm_rope_args(sides, inv_freq, wq, wk, norm, positions, pos0):
+    """Checks a call's sides [(name, tensor, [(name, tensor like it)])] for q and k: the sizes, the
+    type's code and the device."""
     torch = _torch()
-    if all(p[1] is None for p in pairs):
+    ref = sides[0][1] if sides[0][1] is not None else sides[1][1]
+    if ref is None:
         raise ValueError("q or k must be given")
-    ref = next(p[1] for p in pairs if p[1] is not None)
-    B, N, _, D = _bnhd(ref, "q/k")
-    for name, t, *others in pairs:
+    if ref.dim() != 4:
+        raise ValueError("q and k must be [B,N,H,D]")
+    B, N, _, D = ref.shape
+    dt, dev = ref.dtype, ref.get_device()
+    heads = []
+    for name, t, likes in sides:
         if t is None:
-            if any(o is not None for _, o in others):
+            if any(o is not None for _, o in likes):
                 raise ValueError(f"{name} must be given with its output or gradient")
+            heads.append(0)
             continue
-        if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N or t.shape[3] != D:
-            raise ValueError("q and k must be [B,N,H,D] with the same B, N and D")
-        _shaped(t, name, t.shape, ref.dtype)
-        for oname, o in others:
-            _shaped(o, oname, t.shape, ref.dtype)
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            if not norm:
-                raise ValueError(f"{name} is only used with norm=True")
-            _shaped(w, name, (D,), ref.dtype)
-    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous fp32 vector of R/2 frequencies")
+        H = t.shape[2] if t.dim() == 4 else 1
+        shape = (B, N, H, D)
+        _fit(t, name, shape, dt, dev)
+        for like, o in likes:
+            if o is None:
+                raise ValueError(f"{like} must be given with {name}")
+            _fit(o, like, shape, dt, dev)
+        heads.append(H)
+    if wq is not None or wk is not None:
+        if not norm:
+            raise ValueError("wq and wk are only used with norm=True")
+        for name, w in (("wq", wq), ("wk", wk)):
+            if w is not None:
+                _fit(w, name, (D,), dt, dev)
+    _fit(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, dev)
     if positions is not None:
-        _shaped(positions, "positions", (B, N), torch.int32)
+        _fit(positions, "positions", (B, N), torch.int32, dev)
     if not -2 ** 31 <= pos0 < 2 ** 31 - N:
         raise ValueError("pos0 is outside the range of positions")
-    heads = [0 if p[1] is None else p[1].shape[2] for p in pairs]
-    return ref, B, N, heads[0], heads[1], D, 2 * inv_freq.numel()
+    return B, N, heads[0], heads[1], D, 2 * inv_freq.numel(), _dtype_code(ref, "q/k", True), dev
 
 
 def qk_norm_rope_fwd(q, k, q_out, k_out, inv_freq, wq=None, wk=None, norm=True, eps=1e-6, positions=None, pos0=0,
@@ -492,12 +515,11 @@ def qk_norm_rope_fwd(q, k, q_out, k_out, inv_freq, wq=None, wk=None, norm=True, 
     embedding of its first 2*len(inv_freq) elements, in one pass, into q_out and k_out (which
     may be q and k).  q with q_out, or k with k_out, may be None.  wq, wk [D] (None: 1);
     positions [B,N] int32 (None: pos0 + row); bf16, fp16 or fp32."""
-    ref, B, N, Hq, Hk, D, R = _norm_rope_args([("q", q, ("q_out", q_out)), ("k", k, ("k_out", k_out))], inv_freq, wq,
-                                              wk, norm, positions, pos0)
-    dt = _dtype_code(ref, "q/k", True)
-    dev = _one_device(q=q, k=k, q_out=q_out, k_out=k_out, wq=wq, wk=wk, positions=positions, inv_freq=inv_freq)
-    _call_on(dev, "qk_norm_rope_fwd", stream, _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(inv_freq),
-             _ptr(q_out), _ptr(k_out), B, N, Hq, Hk, D, R, int(interleaved), int(norm), eps, attn_factor, pos0, dt)
+    B, N, Hq, Hk, D, R, dt, dev = _norm_rope_args((("q", q, (("q_out", q_out),)), ("k", k, (("k_out", k_out),))),
+                                                  inv_freq, wq, wk, norm, positions, pos0)
+    _call_on(dev, "qk_norm_rope_fwd", stream, _adr(q), _adr(k), _adr(wq), _adr(wk), _adr(positions),
+             inv_freq.data_ptr(), _adr(q_out), _adr(k_out), B, N, Hq, Hk, D, R, bool(interleaved), bool(norm), eps,
+             attn_factor, pos0, dt)
 
 
 def qk_norm_rope_bwd_workspace_bytes(D):
@@ -509,29 +531,23 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, inv_freq, wq=None, wk=None, d
     """Backward of qk_norm_rope_fwd: dq, dk (which may be dq_out, dk_out) and, where given, dwq, dwk
     [D].  q, k are the forward's inputs (norm=False: may be None).  workspace: a uint8 device
     tensor of qk_norm_rope_bwd_workspace_bytes(D) bytes, needed with dwq or dwk."""
-    sides = [("dq_out", dq_out, ("dq", dq)), ("dk_out", dk_out, ("dk", dk))]
     if norm:
-        for s, name, x in ((0, "q", q), (1, "k", k)):
-            sides[s] += ((name, x),)
-    ref, B, N, Hq, Hk, D, R = _norm_rope_args(sides, inv_freq, wq, wk, norm, positions, pos0)
-    dt = _dtype_code(ref, "q/k", True)
-    for name, d, g in (("dwq", dwq, dq), ("dwk", dwk, dk)):
-        if d is not None:
-            if not norm or g is None:
-                raise ValueError(f"{name} needs norm=True and its side's gradient")
-            _shaped(d, name, (D,), ref.dtype)
-    if dwq is not None or dwk is not None:
-        _workspace(workspace)
+        sides = (("dq_out", dq_out, (("dq", dq), ("q", q))), ("dk_out", dk_out, (("dk", dk), ("k", k))))
     else:
-        workspace = None
-    if not norm:
         q = k = None
-    dev = _one_device(q=q, k=k, dq_out=dq_out, dk_out=dk_out, dq=dq, dk=dk, wq=wq, wk=wk, dwq=dwq, dwk=dwk,
-                      positions=positions, inv_freq=inv_freq, workspace=workspace)
-    _call_on(dev, "qk_norm_rope_bwd", stream, _ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(wq), _ptr(wk),
-             _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), B, N, Hq, Hk, D, R,
-             int(interleaved), int(norm), eps, attn_factor, pos0, dt, _ptr(workspace),
-             0 if workspace is None else workspace.numel() * workspace.element_size())
+        sides = (("dq_out", dq_out, (("dq", dq),)), ("dk_out", dk_out, (("dk", dk),)))
+    B, N, Hq, Hk, D, R, dt, dev = _norm_rope_args(sides, inv_freq, wq, wk, norm, positions, pos0)
+    ws, ws_bytes = None, 0
+    if dwq is not None or dwk is not None:
+        for name, d, g in (("dwq", dwq, dq), ("dwk", dwk, dk)):
+            if d is not None:
+                if not norm or g is None:
+                    raise ValueError(f"{name} needs norm=True and its side's gradient")
+                _fit(d, name, (D,), g.dtype, dev)
+        ws, ws_bytes = _scratch(workspace, dev)
+    _call_on(dev, "qk_norm_rope_bwd", stream, _adr(q), _adr(k), _adr(dq_out), _adr(dk_out), _adr(wq), _adr(wk),
+             _adr(positions), inv_freq.data_ptr(), _adr(dq), _adr(dk), _adr(dwq), _adr(dwk), B, N, Hq, Hk, D, R,
+             bool(interleaved), bool(norm), eps, attn_factor, pos0, dt, ws, ws_bytes)
 
 
 def s2attn_tree_mask(parents, mask, depth=None, stream=None):
@@ -541,28 +557,31 @@ def s2attn_tree_mask(parents, mask, depth=None, stream=None):
     if parents.dim() != 2:
         raise ValueError("parents must be [B,M]")
     B, M = parents.shape
-    _shaped(parents, "parents", (B, M), torch.int32)
-    _shaped(mask, "mask", (B, M, (M + 63) // 64), torch.int64)
+    dev = parents.get_device()
+    _fit(parents, "parents", (B, M), torch.int32, dev)
+    _fit(mask, "mask", (B, M, (M + 63) // 64), torch.int64, dev)
     if depth is not None:
-        _shaped(depth, "depth", (B, M), torch.int32)
-    dev = _one_device(parents=parents, mask=mask, depth=depth)
-    _call_on(dev, "s2attn_tree_mask", stream, _ptr(parents), _ptr(mask), _ptr(depth), B, M)
+        _fit(depth, "depth", (B, M), torch.int32, dev)
+    _call_on(dev, "s2attn_tree_mask", stream, parents.data_ptr(), mask.data_ptr(), _adr(depth), B, M)
 
 
 def s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D):
     return int(capi().s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D))
 
 
-def _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype):
-    torch = _torch()
+def _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype, dev):
+    """Checks a paged cache; its pages, page size and table width."""
+    int32 = _torch().int32
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_pages must be [n_pages,page_size,Hkv,D] and page_table [B,table_width]")
-    n_pages, page_size = k_pages.shape[:2]
-    _shaped(k_pages, "k_pages", (n_pages, page_size, Hkv, D), dtype)
-    _shaped(v_pages, "v_pages", (n_pages, page_size, Hkv, D), dtype)
-    _shaped(page_table, "page_table", (B, page_table.shape[1]), torch.int32)
-    _shaped(cache_len, "cache_len", (B,), torch.int32)
-    return n_pages, page_size, page_table.shape[1]
+    n_pages, page_size, _, _ = k_pages.shape
+    shape = (n_pages, page_size, Hkv, D)
+    _fit(k_pages, "k_pages", shape, dtype, dev)
+    _fit(v_pages, "v_pages", shape, dtype, dev)
+    width = page_table.shape[1]
+    _fit(page_table, "page_table", (B, width), int32, dev)
+    _fit(cache_len, "cache_len", (B,), int32, dev)
+    return n_pages, page_size, width
 
 
 def s2attn_tree_decode(q, k_new, v_new, k_pages, v_pages, page_table, cache_len, o, lse, workspace, tree_mask=None,
@@ -574,26 +593,26 @@ def s2attn_tree_decode(q, k_new, v_new, k_pages, v_pages, page_table, cache_len,
     other rows of o and lse stay.  bf16 or fp16.  workspace: a uint8 device tensor of
     s2attn_tree_decode_workspace_bytes(B, M, H, Hkv, D) bytes, one per call in flight."""
     torch = _torch()
-    B, M, H, D = _bnhd(q, "q")
-    if k_new.dim() != 4:
-        raise ValueError("k_new must be [B,M,Hkv,D]")
+    if q.dim() != 4 or k_new.dim() != 4:
+        raise ValueError("q must be [B,M,H,D] and k_new [B,M,Hkv,D]")
+    B, M, H, D = q.shape
     Hkv = k_new.shape[2]
-    dt = _dtype_code(q, "q", False)
-    _shaped(k_new, "k_new", (B, M, Hkv, D), q.dtype)
-    _shaped(v_new, "v_new", (B, M, Hkv, D), q.dtype)
-    n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, q.dtype)
-    _shaped(o, "o", (B, M, H, D), q.dtype)
-    _shaped(lse, "lse", (B, H, M), torch.float32)
+    dtype, dev = q.dtype, q.get_device()
+    code = _dtype_code(q, "q", False)
+    _fit(q, "q", (B, M, H, D), dtype, dev)
+    _fit(o, "o", (B, M, H, D), dtype, dev)
+    _fit(k_new, "k_new", (B, M, Hkv, D), dtype, dev)
+    _fit(v_new, "v_new", (B, M, Hkv, D), dtype, dev)
+    n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype, dev)
+    _fit(lse, "lse", (B, H, M), torch.float32, dev)
     if tree_mask is not None:
-        _shaped(tree_mask, "tree_mask", (B, M, (M + 63) // 64), torch.int64)
+        _fit(tree_mask, "tree_mask", (B, M, (M + 63) // 64), torch.int64, dev)
     if new_len is not None:
-        _shaped(new_len, "new_len", (B,), torch.int32)
-    _workspace(workspace)
-    dev = _one_device(q=q, k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
-                      cache_len=cache_len, o=o, lse=lse, tree_mask=tree_mask, new_len=new_len, workspace=workspace)
-    _call_on(dev, "s2attn_tree_decode", stream, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
-             _ptr(page_table), _ptr(cache_len), _ptr(new_len), _ptr(tree_mask), _ptr(o), _ptr(lse), B, M, H, Hkv, D,
-             n_pages, page_size, width, dt, _ptr(workspace), workspace.numel() * workspace.element_size())
+        _fit(new_len, "new_len", (B,), torch.int32, dev)
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call_on(dev, "s2attn_tree_decode", stream, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
+             v_pages.data_ptr(), page_table.data_ptr(), cache_len.data_ptr(), _adr(new_len), _adr(tree_mask),
+             o.data_ptr(), lse.data_ptr(), B, M, H, Hkv, D, n_pages, page_size, width, code, ws, ws_bytes)
 
 
 def s2attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, rows=None, n_rows=None, stream=None):
@@ -601,23 +620,25 @@ def s2attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, r
     rows[b][j] goes to position cache_len[b] + j.  rows [B,A] int32 (None: row j, all M);
     n_rows [B] int32 (None: A).  cache_len is not changed.  bf16, fp16 or fp32."""
     torch = _torch()
-    B, M, Hkv, D = _bnhd(k_new, "k_new")
+    if k_new.dim() != 4:
+        raise ValueError("k_new must be [B,M,Hkv,D]")
+    B, M, Hkv, D = k_new.shape
+    dtype, dev = k_new.dtype, k_new.get_device()
     _dtype_code(k_new, "k_new", True)
-    _shaped(v_new, "v_new", (B, M, Hkv, D), k_new.dtype)
-    n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, k_new.dtype)
+    _fit(k_new, "k_new", (B, M, Hkv, D), dtype, dev)
+    _fit(v_new, "v_new", (B, M, Hkv, D), dtype, dev)
+    n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype, dev)
     A = M
     if rows is not None:
         if rows.dim() != 2:
             raise ValueError("rows must be [B,A]")
         A = rows.shape[1]
-        _shaped(rows, "rows", (B, A), torch.int32)
+        _fit(rows, "rows", (B, A), torch.int32, dev)
     if n_rows is not None:
-        _shaped(n_rows, "n_rows", (B,), torch.int32)
-    dev = _one_device(k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
-                      cache_len=cache_len, rows=rows, n_rows=n_rows)
-    _call_on(dev, "s2attn_cache_append", stream, _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
-             _ptr(page_table), _ptr(cache_len), _ptr(rows), _ptr(n_rows), B, M, A, Hkv, D, n_pages, page_size, width,
-             k_new.element_size())
+        _fit(n_rows, "n_rows", (B,), torch.int32, dev)
+    _call_on(dev, "s2attn_cache_append", stream, k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
+             v_pages.data_ptr(), page_table.data_ptr(), cache_len.data_ptr(), _adr(rows), _adr(n_rows), B, M, A, Hkv, D,
+             n_pages, page_size, width, k_new.element_size())
 
 
 def s2attn_cache_copy_pages(pools, pairs, stream=None):
@@ -627,20 +648,22 @@ def s2attn_cache_copy_pages(pools, pairs, stream=None):
     if not pools:
         raise ValueError("pools must be a non-empty list")
     ref = pools[0]
-    if ref.dim() < 2:
+    shape, dtype, dev = ref.shape, ref.dtype, ref.get_device()
+    if len(shape) < 2:
         raise ValueError("a pool must be [n_pages, ...]")
-    for i, t in enumerate(pools):
-        _shaped(t, f"pools[{i}]", ref.shape, ref.dtype)
-    dev = _one_device(**{f"pools[{i}]": t for i, t in enumerate(pools)})
-    n_pages = ref.shape[0]
-    flat = []
-    for src, dst in pairs:
-        if not (0 <= src < n_pages and 0 <= dst < n_pages):
-            raise ValueError(f"pair ({src}, {dst}) is outside [0, {n_pages})")
-        flat += (int(src), int(dst))
-    _call_on(dev, "s2attn_cache_copy_pages", stream, _ptr_array(pools), len(pools), (ctypes.c_int * len(flat))(*flat),
-             len(pairs), n_pages, ref.numel() // max(n_pages, 1) * ref.element_size())
-
+    for t in pools:
+        _fit(t, "every pool", shape, dtype, dev)
+    flat = array.array("i", bytes(8 * len(pairs)))
+    if len(pairs):
+        src, dst = zip(*pairs, strict=True)      # a pair of any other length raises ValueError
+        try:
+            flat[0::2], flat[1::2] = array.array("i", src), array.array("i", dst)
+        except OverflowError:
+            raise ValueError("a page number does not fit 32 bits") from None
+    n_pages = shape[0]
+    _call_on(dev, "s2attn_cache_copy_pages", stream, _ptr_array(pools), len(pools),
+             (ctypes.c_int * len(flat)).from_buffer(flat) if len(flat) else None, len(pairs), n_pages,
+             ref.numel() // max(n_pages, 1) * ref.element_size())
 
 
 def get_device_error():

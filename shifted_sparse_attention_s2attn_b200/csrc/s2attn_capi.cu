@@ -6,10 +6,10 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <cstring>
 #include <map>
 #include <mutex>
-#include <new>
 #include <tuple>
 #include <vector>
 
@@ -818,17 +818,17 @@ int s2attn_cache_copy_pages(void* const* pools, int n_pools, const int* pairs, i
     if (!aligned16(pools[i])) return S2ATTN_ERR_INVALID_ARG;
   if (n_pairs == 0) return S2ATTN_OK;
   if (!pairs || n_pairs > n_pages) return S2ATTN_ERR_INVALID_ARG;   // each pair writes a page of its own
-  int* dst = new (std::nothrow) int[n_pairs];
-  if (!dst) return S2ATTN_ERR_INVALID_ARG;
+  // one bit a page: written by a pair so far
+  uint32_t* written = static_cast<uint32_t*>(std::calloc((size_t)n_pages / 32 + 1, sizeof(uint32_t)));
+  if (!written) return S2ATTN_ERR_INVALID_ARG;
   bool ok = true;
-  for (int i = 0; i < n_pairs; ++i) {
-    ok = ok && pairs[2 * i] >= 0 && pairs[2 * i] < n_pages && pairs[2 * i + 1] >= 0 && pairs[2 * i + 1] < n_pages;
-    dst[i] = pairs[2 * i + 1];
+  for (int i = 0; i < n_pairs && ok; ++i) {
+    const int src = pairs[2 * i], dst = pairs[2 * i + 1];
+    ok = src >= 0 && src < n_pages && dst >= 0 && dst < n_pages && !(written[dst / 32] >> (dst % 32) & 1u);
+    if (ok) written[dst / 32] |= 1u << (dst % 32);
   }
-  std::sort(dst, dst + n_pairs);
-  for (int i = 1; i < n_pairs; ++i) ok = ok && dst[i] != dst[i - 1];
-  for (int i = 0; i < n_pairs; ++i) ok = ok && !std::binary_search(dst, dst + n_pairs, pairs[2 * i]);
-  delete[] dst;
+  for (int i = 0; i < n_pairs && ok; ++i) ok = !(written[pairs[2 * i] / 32] >> (pairs[2 * i] % 32) & 1u);
+  std::free(written);
   if (!ok) return S2ATTN_ERR_INVALID_ARG;
   return cuda_status(s2::launch_cache_copy(pools, n_pools, pairs, n_pairs, (long long)page_bytes,
                                            static_cast<cudaStream_t>(stream)));
