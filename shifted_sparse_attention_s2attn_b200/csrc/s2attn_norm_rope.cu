@@ -33,6 +33,7 @@ namespace s2 {
 namespace nr {
 
 constexpr int THREADS = 256;
+constexpr int FWD_CTAS = 6, BWD_CTAS = 4;    // CTAs an SM, at most
 constexpr int MAX_TAB = 4096;   // (cos, sin) pairs a CTA holds: 32 KB
 
 struct Side {                   // q or k
@@ -43,6 +44,10 @@ struct Side {                   // q or k
   int H;
   int ctas;                     // CTAs that take this side's tiles
   int tile;                     // tokens of a tile
+  // the CTA's lane groups take `toks` tokens at a time, `gp` groups to a token, each `per` of its
+  // heads one after another (so that a lane keeps the token's angles in registers)
+  int gp, per, toks;
+  long long next_head, next_tok;   // elements from a row to the group's next one
   float* part;                  // backward with a weight: [ctas][D] partial sums
 };
 
@@ -54,58 +59,57 @@ struct Params {
   float eps, af;
 };
 
+// Eight elements as loaded, and as fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(Raw<T>& r, const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, float2 (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[2 * i] = make_float2(__uint_as_float(r.v[i].x), __uint_as_float(r.v[i].y));
+    f[2 * i + 1] = make_float2(__uint_as_float(r.v[i].z), __uint_as_float(r.v[i].w));
   }
 }
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float (&f)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float2 (&f)[4]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<__half>& r, float2 (&f)[4]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]);
+__device__ __forceinline__ void store8(T* p, const float2 (&f)[4]);
 template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&f)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store8<float>(float* p, const float2 (&f)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
 template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float2 (&f)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[i].x, f[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <>
-__device__ __forceinline__ void store8<__half>(__half* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8<__half>(__half* p, const float2 (&f)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    const __half2 v = __floats2half2_rn(f[i].x, f[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -123,37 +127,55 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Turns the pairs of chunks c0 (a) and c1 (b); cs is the token's (cos, sin) row.
-// BACK turns by the negated angles.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The cosines and sines of a lane's pairs: of frequencies 8 c0 .. 8 c0 + 7 (half layout), or of
+// 4 c0 .. 4 c0 + 3 and 4 c1 .. 4 c1 + 3 (interleaved).
+struct Angles {
+  float2 c[4], s[4];
+};
+__device__ __forceinline__ void get_angles(Angles& g, const float* cosr, const float* sinr, int c0, int c1,
+                                           int interleaved) {
+  const int f0 = interleaved ? 4 * c0 : 8 * c0, f1 = interleaved ? 4 * c1 : 8 * c0 + 4;
+  const float4 a = *reinterpret_cast<const float4*>(cosr + f0), b = *reinterpret_cast<const float4*>(cosr + f1);
+  const float4 u = *reinterpret_cast<const float4*>(sinr + f0), v = *reinterpret_cast<const float4*>(sinr + f1);
+  g.c[0] = make_float2(a.x, a.y), g.c[1] = make_float2(a.z, a.w);
+  g.c[2] = make_float2(b.x, b.y), g.c[3] = make_float2(b.z, b.w);
+  g.s[0] = make_float2(u.x, u.y), g.s[1] = make_float2(u.z, u.w);
+  g.s[2] = make_float2(v.x, v.y), g.s[3] = make_float2(v.z, v.w);
+}
+
+// Turns the pairs of chunks c0 (a) and c1 (b); BACK by the negated angles.
+__device__ __forceinline__ float2 turn_one(float2 x, float c, float s) {
+  return make_float2(x.x * c - x.y * s, x.y * c + x.x * s);
+}
 template <bool BACK>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float2* cs, int c0, int c1, int interleaved) {
+__device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const Angles& g, int interleaved) {
   if (interleaved) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float2 u = cs[4 * c0 + p], v = cs[4 * c1 + p];
-      const float su = BACK ? -u.y : u.y, sv = BACK ? -v.y : v.y;
-      const float a0 = a[2 * p], a1 = a[2 * p + 1], b0 = b[2 * p], b1 = b[2 * p + 1];
-      a[2 * p] = a0 * u.x - a1 * su;
-      a[2 * p + 1] = a1 * u.x + a0 * su;
-      b[2 * p] = b0 * v.x - b1 * sv;
-      b[2 * p + 1] = b1 * v.x + b0 * sv;
+    for (int p = 0; p < 2; ++p) {
+      const float2 s = BACK ? make_float2(-g.s[p].x, -g.s[p].y) : g.s[p];
+      const float2 t = BACK ? make_float2(-g.s[p + 2].x, -g.s[p + 2].y) : g.s[p + 2];
+      a[2 * p] = turn_one(a[2 * p], g.c[p].x, s.x);
+      a[2 * p + 1] = turn_one(a[2 * p + 1], g.c[p].y, s.y);
+      b[2 * p] = turn_one(b[2 * p], g.c[p + 2].x, t.x);
+      b[2 * p + 1] = turn_one(b[2 * p + 1], g.c[p + 2].y, t.y);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 u = cs[8 * c0 + e];
-      const float s = BACK ? -u.y : u.y;
-      const float x = a[e], y = b[e];
-      a[e] = x * u.x - y * s;
-      b[e] = y * u.x + x * s;
+    for (int e = 0; e < 4; ++e) {
+      const float2 s = g.s[e], ns = make_float2(-s.x, -s.y);
+      const float2 x = a[e], y = b[e];
+      a[e] = __ffma2_rn(x, g.c[e], __fmul2_rn(y, BACK ? s : ns));
+      b[e] = __ffma2_rn(y, g.c[e], __fmul2_rn(x, BACK ? ns : s));
     }
   }
 }
 
 // LPR lanes hold a row (a power of two >= D/16; lanes beyond D/16 idle).
 template <typename T, int LPR, bool BWD>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float2 tab[];                  // [tile][R/2]
+__global__ void __launch_bounds__(THREADS, BWD ? 2 : 3) norm_rope_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) float tab[];     // cos [tile][R/2], then sin
   constexpr int ROWS = THREADS / LPR;              // rows of one step of the CTA
   const int side = (int)blockIdx.x < p.s[0].ctas ? 0 : 1;
   const Side& s = p.s[side];
@@ -164,109 +186,146 @@ __global__ void __launch_bounds__(THREADS) norm_rope_kernel(const __grid_constan
   const bool rot = lane < R / 16;
   const int c0 = rot ? lane : R / 8 + 2 * (lane - R / 16);
   const int c1 = rot ? lane + R / 16 : c0 + 1;
-  float w0[8], w1[8];
+  float2 w0[4], w1[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w0[e] = w1[e] = 1.0f;
+  for (int e = 0; e < 4; ++e) w0[e] = w1[e] = both(1.0f);
   if (s.w && has) {
-    load8(static_cast<const T*>(s.w) + 8 * c0, w0);
-    load8(static_cast<const T*>(s.w) + 8 * c1, w1);
+    Raw<T> r;
+    load_raw(r, static_cast<const T*>(s.w) + 8 * c0);
+    unpack(r, w0);
+    load_raw(r, static_cast<const T*>(s.w) + 8 * c1);
+    unpack(r, w1);
   }
-  float dw0[8], dw1[8];
+  float2 dw0[4], dw1[4];
   if (BWD) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw0[e] = dw1[e] = 0.0f;
+    for (int e = 0; e < 4; ++e) dw0[e] = dw1[e] = both(0.0f);
   }
   const float inv_d = 1.0f / (float)D;
-  const long long n_tiles = ((long long)p.tokens + s.tile - 1) / s.tile;
-  for (long long tl = cta; tl < n_tiles; tl += s.ctas) {
-    const int tok0 = (int)(tl * s.tile);
-    const int n_tok = min(s.tile, p.tokens - tok0);
+  // this CTA's tokens, equal shares; a tile of them has its cos and sin in shared memory
+  const int tok_begin = (int)((long long)p.tokens * cta / s.ctas);
+  const int tok_end = (int)((long long)p.tokens * (cta + 1) / s.ctas);
+  const bool need_x = !BWD || p.norm;
+  for (int tok0 = tok_begin; tok0 < tok_end; tok0 += s.tile) {
+    const int n_tok = min(s.tile, tok_end - tok0);
+    const size_t base = (size_t)tok0 * H * D;
+    const T* x = static_cast<const T*>(s.x) + base;
+    const T* dy = static_cast<const T*>(s.dy) + base;
+    T* y = static_cast<T*>(s.y) + base;
+    // a row's loads go out one step before it is worked on, the first ones before the angles
+    Raw<T> xa, xb, ya, yb;
+    auto fetch = [&](int tok, size_t off) {
+      if (!has || tok >= n_tok) return;
+      if (need_x) {
+        load_raw(xa, x + off + 8 * c0);
+        load_raw(xb, x + off + 8 * c1);
+      }
+      if (BWD) {
+        load_raw(ya, dy + off + 8 * c0);
+        load_raw(yb, dy + off + 8 * c1);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) xa.v[i] = xb.v[i] = ya.v[i] = yb.v[i] = make_uint4(0, 0, 0, 0);
+    int tok = row0 / s.gp, k = 0;
+    size_t off = ((size_t)tok * H + row0 % s.gp) * D;
+    fetch(tok, off);
     __syncthreads();
+    float* sin_tab = tab + n_tok * half;
     for (int i = threadIdx.x; i < n_tok * half; i += THREADS) {
       const int tk = i / half, f = i - tk * half;
       const int pos = p.pos ? p.pos[tok0 + tk] : p.pos0 + (tok0 + tk) % p.N;
       const double turns = (double)pos * (double)p.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
       float sn, cn;
       sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
-      tab[i] = make_float2(cn * p.af, sn * p.af);
+      tab[i] = cn * p.af;
+      sin_tab[i] = sn * p.af;
     }
     __syncthreads();
-    const int n_rows = n_tok * H;
-    const size_t base = (size_t)tok0 * H * D;
-    for (int r0 = 0; r0 < n_rows; r0 += ROWS) {   // the same trip count for every lane
-      const int r = r0 + row0;
-      const bool live = has && r < n_rows;
-      const size_t off = base + (size_t)r * D;
-      float a[8], b[8], ga[8], gb[8];
+    Angles g;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = b[e] = ga[e] = gb[e] = 0.0f;
-      if (live) {
-        if (!BWD || p.norm) {
-          load8(static_cast<const T*>(s.x) + off + 8 * c0, a);
-          load8(static_cast<const T*>(s.x) + off + 8 * c1, b);
-        }
-        if (BWD) {
-          load8(static_cast<const T*>(s.dy) + off + 8 * c0, ga);
-          load8(static_cast<const T*>(s.dy) + off + 8 * c1, gb);
-        }
+    for (int e = 0; e < 4; ++e) g.c[e] = both(1.0f), g.s[e] = both(0.0f);
+    const int steps = (n_tok + s.toks - 1) / s.toks * s.per;   // the same for every lane
+    for (int i = 0; i < steps; ++i) {
+      const bool live = has && tok < n_tok;
+      const size_t at = off;
+      float2 a[4], b[4], ga[4], gb[4];
+      unpack(xa, a);
+      unpack(xb, b);
+      if (BWD) {
+        unpack(ya, ga);
+        unpack(yb, gb);
       }
-      const float2* cs = tab + (live ? r / H : 0) * half;
+      if (k == 0 && rot && live) get_angles(g, tab + tok * half, sin_tab + tok * half, c0, c1, p.interleaved);
+      if (++k == s.per) {
+        k = 0;
+        tok += s.toks;
+        off += s.next_tok;
+      } else {
+        off += s.next_head;
+      }
+      fetch(tok, off);
       float rstd = 1.0f;
       if (p.norm) {
-        float ss = 0.0f;
+        float2 ss = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
-        rstd = rsqrtf(row_sum<LPR>(ss) * inv_d + p.eps);
+        for (int e = 0; e < 4; ++e) ss = __ffma2_rn(a[e], a[e], __ffma2_rn(b[e], b[e], ss));
+        rstd = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_d + p.eps);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {   // xhat
+          a[e] = __fmul2_rn(a[e], both(rstd));
+          b[e] = __fmul2_rn(b[e], both(rstd));
+        }
       }
       if (!BWD) {
         if (p.norm) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] = a[e] * rstd * w0[e];
-            b[e] = b[e] * rstd * w1[e];
+          for (int e = 0; e < 4; ++e) {
+            a[e] = __fmul2_rn(a[e], w0[e]);
+            b[e] = __fmul2_rn(b[e], w1[e]);
           }
         }
-        if (rot) turn<false>(a, b, cs, c0, c1, p.interleaved);
+        if (rot) turn<false>(a, b, g, p.interleaved);
         if (live) {
-          store8(static_cast<T*>(s.y) + off + 8 * c0, a);
-          store8(static_cast<T*>(s.y) + off + 8 * c1, b);
+          store8(y + at + 8 * c0, a);
+          store8(y + at + 8 * c1, b);
         }
       } else {
-        if (rot) turn<true>(ga, gb, cs, c0, c1, p.interleaved);
+        if (rot) turn<true>(ga, gb, g, p.interleaved);
         if (p.norm) {
-          float dot = 0.0f;
+          float2 dot2 = both(0.0f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] *= rstd;   // xhat
-            b[e] *= rstd;
-            dw0[e] = fmaf(ga[e], a[e], dw0[e]);
-            dw1[e] = fmaf(gb[e], b[e], dw1[e]);
-            ga[e] *= w0[e];
-            gb[e] *= w1[e];
-            dot = fmaf(ga[e], a[e], fmaf(gb[e], b[e], dot));
+          for (int e = 0; e < 4; ++e) {
+            if (live) {     // behind its last row a lane holds that row's values still
+              dw0[e] = __ffma2_rn(ga[e], a[e], dw0[e]);
+              dw1[e] = __ffma2_rn(gb[e], b[e], dw1[e]);
+            }
+            ga[e] = __fmul2_rn(ga[e], w0[e]);
+            gb[e] = __fmul2_rn(gb[e], w1[e]);
+            dot2 = __ffma2_rn(ga[e], a[e], __ffma2_rn(gb[e], b[e], dot2));
           }
-          dot = row_sum<LPR>(dot) * inv_d;
+          const float dot = row_sum<LPR>(dot2.x + dot2.y) * inv_d;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ga[e] = rstd * (ga[e] - a[e] * dot);
-            gb[e] = rstd * (gb[e] - b[e] * dot);
+          for (int e = 0; e < 4; ++e) {
+            ga[e] = __fmul2_rn(both(rstd), __ffma2_rn(a[e], both(-dot), ga[e]));
+            gb[e] = __fmul2_rn(both(rstd), __ffma2_rn(b[e], both(-dot), gb[e]));
           }
         }
         if (live) {
-          store8(static_cast<T*>(s.y) + off + 8 * c0, ga);
-          store8(static_cast<T*>(s.y) + off + 8 * c1, gb);
+          store8(y + at + 8 * c0, ga);
+          store8(y + at + 8 * c1, gb);
         }
       }
     }
   }
   if (BWD && s.part) {   // the CTA's sums, rows in order
-    float* red = reinterpret_cast<float*>(tab);    // [ROWS][D]
+    float* red = tab;                              // [ROWS][D]
     __syncthreads();
     if (has) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        red[row0 * D + 8 * c0 + e] = dw0[e];
-        red[row0 * D + 8 * c1 + e] = dw1[e];
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<float2*>(red + row0 * D + 8 * c0 + 2 * e) = dw0[e];
+        *reinterpret_cast<float2*>(red + row0 * D + 8 * c1 + 2 * e) = dw1[e];
       }
     }
     __syncthreads();
@@ -304,7 +363,7 @@ __global__ void __launch_bounds__(256) dw_sum_kernel(const __grid_constant__ Sum
 size_t smem_bytes(const Params& p, int lpr, bool bwd) {
   size_t tab = 0;
   for (int i = 0; i < 2; ++i)
-    if (p.s[i].ctas) tab = std::max(tab, (size_t)p.s[i].tile * (p.R / 2) * sizeof(float2));
+    if (p.s[i].ctas) tab = std::max(tab, (size_t)p.s[i].tile * (p.R / 2) * 2 * sizeof(float));
   const size_t red = bwd ? (size_t)(THREADS / lpr) * p.D * sizeof(float) : 0;
   return std::max(tab, red);
 }
@@ -331,8 +390,8 @@ cudaError_t launch_type(const Params& p, bool bwd, cudaStream_t st) {
   }
 }
 
-// Tokens of a tile and CTAs of each side.  A tile has about four steps of rows so that the
-// cos/sin work is shared by many rows; with few tokens it shrinks until every SM has one.
+// CTAs of each side and the tokens of a tile.  A CTA should have at least a few steps of rows to
+// share its cos and sin among, unless there are too few tokens to give every SM one.
 void plan(Params& p, int n_sm, int max_ctas) {
   const int rows = THREADS / lanes(p.D);
   const int heads = p.s[0].H + p.s[1].H;
@@ -342,14 +401,23 @@ void plan(Params& p, int n_sm, int max_ctas) {
       s.ctas = 0;
       continue;
     }
-    long long tile = (4LL * rows + s.H - 1) / s.H;
-    const long long share = std::max(1LL, (long long)n_sm * s.H / heads);
-    tile = std::min(tile, ((long long)p.tokens + share - 1) / share);
-    if (p.R) tile = std::min(tile, (long long)MAX_TAB / (p.R / 2));
-    s.tile = (int)std::max(1LL, tile);
-    const long long tiles = ((long long)p.tokens + s.tile - 1) / s.tile;
-    const long long cap = std::max(1LL, (long long)max_ctas * s.H / heads);
-    s.ctas = (int)std::min(tiles, cap);
+    const long long tile = std::max(1LL, 4LL * rows / s.H);          // tokens of four steps
+    const long long share = std::max(1LL, (long long)max_ctas * s.H / heads);
+    const long long one_each = std::max(1LL, 4LL * n_sm * s.H / heads);
+    const long long least = std::max(1LL, (long long)rows / s.H);    // tokens of one step
+    long long ctas = std::max(((long long)p.tokens + tile - 1) / tile,
+                              std::min(((long long)p.tokens + least - 1) / least, one_each));
+    s.ctas = (int)std::min(ctas, share);
+    const long long toks = ((long long)p.tokens + s.ctas - 1) / s.ctas;
+    s.tile = (int)(p.R ? std::min(toks, (long long)MAX_TAB / (p.R / 2)) : toks);
+    // at least two heads a group where there are two: neighbouring groups then read neighbouring
+    // rows, and a step of the CTA spans few tokens
+    s.gp = 1;
+    while (s.H % (2 * s.gp) == 0 && s.H / (2 * s.gp) >= 2 && 2 * s.gp <= rows) s.gp *= 2;
+    s.per = s.H / s.gp;
+    s.toks = rows / s.gp;
+    s.next_head = (long long)s.gp * p.D;
+    s.next_tok = (long long)s.toks * s.H * p.D - (s.per - 1) * s.next_head;
   }
 }
 
@@ -376,13 +444,13 @@ cudaError_t launch(const Params& p, int dtype, bool bwd, cudaStream_t st) {
 
 cudaError_t launch_norm_rope_fwd(const NormRopeArgs& a, int n_sm, cudaStream_t st) {
   nr::Params p = nr::make(a);
-  nr::plan(p, n_sm, 16 * n_sm);
+  nr::plan(p, n_sm, nr::FWD_CTAS * n_sm);
   return nr::launch(p, a.dtype, false, st);
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* part, int n_sm, cudaStream_t st) {
   nr::Params p = nr::make(a);
-  nr::plan(p, n_sm, std::min(kNormRopePartials, 4 * n_sm));
+  nr::plan(p, n_sm, std::min(kNormRopePartials, nr::BWD_CTAS * n_sm));
   if (a.dwq && p.s[0].H) p.s[0].part = part;
   if (a.dwk && p.s[1].H) p.s[1].part = part + (size_t)p.s[0].ctas * a.D;
   cudaError_t e = nr::launch(p, a.dtype, true, st);
