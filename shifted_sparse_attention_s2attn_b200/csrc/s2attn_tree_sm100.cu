@@ -314,11 +314,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int b = lane; b < p.B; b += 32) sum += all_tiles(s_len[b], s_new[b], first_tok);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int runs = (int)min((long long)p.J, max(1LL, sum / kTreeMinRun));
+    const int runs = (int)min((long long)p.J, max(1LL, sum >> kTreeMinRunLog2));
     long long w0 = 0, w1 = 0;
-    if (j < runs) {
-      w0 = sum * j / runs;
-      w1 = sum * (j + 1) / runs;
+    if (j < runs) {   // the first sum % runs runs have one tile more
+      const long long each = sum <= 0x7fffffff ? (int)sum / runs : sum / runs, more = sum - each * runs;
+      w0 = each * j + min((long long)j, more);
+      w1 = w0 + each + (j < more ? 1 : 0);
     }
     // the sequence that holds tile w0
     int b0 = 0, t0 = 0;
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           ok = wait_warp(pv_done, (i - 1) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < HD; c += 32) {
             uint32_t rr[32];
             tmem_ld_x32(lane_addr + TM_O + c, rr);
@@ -621,22 +622,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           row_ok && (whole ? in_bounds(orow, 1, (size_t)p.B * p.M * p.H, p.err, (K_TREE << 8) | SITE_STORE)
                            : in_bounds(part, 1, (size_t)gridDim.x * 2 * p.slot_rows, p.err, (K_TREE << 8) | SITE_STORE));
       const float inv = l_run > 0.f || l_run != l_run ? 1.0f / l_run : 0.f;   // a row that sees nothing: 0
-#pragma unroll
+      // (rolled: code that runs once or twice a launch costs its fetch more than its time)
+#pragma unroll 1
       for (int c = 0; c < HD; c += 32) {
         uint32_t rr[32];
         __syncwarp();
         tmem_ld_x32(lane_addr + TM_O + c, rr);
-        for (int e = 0; e < 4; ++e) {
-          for (uint32_t left = fix[e]; left; left &= left - 1) {
-            const int key = e * 32 + __ffs(left) - 1;
-            const uint16_t* v = static_cast<const uint16_t*>(p.v_new) + (((size_t)b * p.M + key) * p.Hkv + kvh) * HD + c;
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float f = unpack16<FP16>(v[x]);
-              if (!isfinite(f)) rr[x] = __float_as_uint(__uint_as_float(rr[x]) + f);
-            }
-          }
-        }
         if (st_ok && whole) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * HD + c);
 #pragma unroll
@@ -653,6 +644,26 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           for (int x = 0; x < 8; ++x)
             dst[x] = make_float4(__uint_as_float(rr[4 * x]), __uint_as_float(rr[4 * x + 1]),
                                  __uint_as_float(rr[4 * x + 2]), __uint_as_float(rr[4 * x + 3]));
+        }
+      }
+      if (st_ok && (fix[0] | fix[1] | fix[2] | fix[3])) {
+        // add the infinities and NaN that clean_v took out, to what this thread has just written
+#pragma unroll 1
+        for (int key = 0; key < 2 * BN; ++key) {
+          const uint32_t w = key < 64 ? (key < 32 ? fix[0] : fix[1]) : (key < 96 ? fix[2] : fix[3]);
+          if (!((w >> (key % 32)) & 1u)) continue;
+          const uint16_t* v = static_cast<const uint16_t*>(p.v_new) + (((size_t)b * p.M + key) * p.Hkv + kvh) * HD;
+#pragma unroll 1
+          for (int c = 0; c < HD; ++c) {
+            const float f = unpack16<FP16>(v[c]);
+            if (isfinite(f)) continue;
+            if (whole) {
+              uint16_t* at = static_cast<uint16_t*>(p.o) + orow * HD + c;
+              *at = (uint16_t)pack16<FP16>(unpack16<FP16>(*at) + f, 0.f);
+            } else {
+              p.part_o[part * HD + c] += f;
+            }
+          }
         }
       }
       if (st_ok) {
@@ -688,72 +699,127 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 }
 
 // o = sum_s 2^(m_s - mx) o_s / sum_s 2^(m_s - mx) l_s over the runs s of the row's sequence;
-// lse = ln2 * (mx + log2 L).  One block per (b, m, h) row: every warp reads all (max, sum)
-// pairs, then takes every fourth run's output.  Rows of a sequence that lay in one run were
-// written by the run.
-constexpr int CW = 4;
+// lse = ln2 * (mx + log2 L).  Rows of a sequence that lay in one run were written by the run.
+// A block takes `rpb` rows: each of its warps one row if the row has few runs, all of them one
+// row after another if it has many (a run's row is 512 B: a warp's lanes take 16 B each).
+constexpr int CW = 8;
+constexpr int kFewRuns = 16;
+
+struct Row {
+  int b, m, h, first, last, u, r;
+  bool mine;    // the row has partials
+};
+__device__ __forceinline__ Row combine_row(const Params& p, long long i) {
+  Row x{};
+  if (i >= (long long)p.B * p.M * p.H) return x;
+  x.h = (int)(i % p.H);
+  x.m = (int)(i / p.H % p.M);
+  x.b = (int)(i / ((long long)p.H * p.M));
+  const int nw = p.new_len ? min(p.new_len[x.b], p.M) : p.M;
+  if (x.m >= nw) return x;
+  const int rt = x.m / p.tok, kvh = x.h / p.group;
+  x.first = max(p.meta[(x.b * p.RT + rt) * 2], 0);
+  x.last = min(p.meta[(x.b * p.RT + rt) * 2 + 1], p.J - 1);
+  x.u = kvh * p.RT + rt;
+  x.r = (x.m - rt * p.tok) * p.group + x.h % p.group;
+  x.mine = x.first < x.last;
+  return x;
+}
+
+template <int HD>
+struct Acc {
+  static constexpr int PER = HD / 32;
+  float v[PER];
+};
+
+// Runs first + from, first + from + step, ... of a row: max over all runs in mx, their sum in L.
+template <int HD>
+__device__ __forceinline__ void combine_runs(const Params& p, const Row& x, int from, int step, int lane, float& mx,
+                                             float& L, Acc<HD>& acc) {
+  constexpr int PER = HD / 32;
+  const int U = p.Hkv * p.RT;
+  // run s: slot 1 of CTA (u, first), slot 0 of the later ones
+  auto row_of = [&](int s) { return (((size_t)s * U + x.u) * 2 + (s == x.first ? 1 : 0)) * p.slot_rows + x.r; };
+  mx = -INFINITY;
+  for (int s = x.first + lane; s <= x.last; s += 32) mx = fmaxf(mx, p.part_ml[row_of(s) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  L = 0.f;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc.v[e] = 0.f;
+  if (mx == -INFINITY) return;
+  for (int s = x.first + lane; s <= x.last; s += 32)
+    L += exp2f(p.part_ml[row_of(s) * 2] - mx) * p.part_ml[row_of(s) * 2 + 1];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll 4
+  for (int s = x.first + from; s <= x.last; s += step) {
+    const size_t row = row_of(s);
+    const float w = exp2f(p.part_ml[row * 2] - mx);
+    alignas(16) float v[PER];
+    if constexpr (PER == 4)
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p.part_o + row * HD + lane * PER);
+    else
+      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p.part_o + row * HD + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc.v[e] = fmaf(w, v[e], acc.v[e]);
+  }
+}
+
 template <int HD, bool FP16>
-__global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_constant__ Params p) {
+__device__ __forceinline__ void combine_store(const Params& p, const Row& x, int lane, float mx, float L,
+                                              const Acc<HD>& acc) {
+  constexpr int PER = HD / 32;
+  const float inv = mx == -INFINITY ? 0.f : 1.0f / L;
+  const size_t orow = ((size_t)x.b * p.M + x.m) * p.H + x.h;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + orow * HD) + lane * (PER / 2);
+#pragma unroll
+  for (int e = 0; e < PER / 2; ++e) dst[e] = pack16<FP16>(acc.v[2 * e] * inv, acc.v[2 * e + 1] * inv);
+  if (lane == 0)
+    p.lse[((size_t)x.b * p.H + x.h) * p.M + x.m] =
+        mx == -INFINITY ? -INFINITY : (mx + log2f(L)) * 0.69314718055994531f;
+}
+
+template <int HD, bool FP16>
+__global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_constant__ Params p, int rpb) {
   constexpr int PER = HD / 32;
   __shared__ float part[CW][HD];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int h = (int)(blockIdx.x % p.H);
-  const int m = (int)((blockIdx.x / p.H) % p.M);
-  const int b = (int)(blockIdx.x / ((unsigned)p.H * p.M));
   // launched as a programmatic dependent of the attention kernel: wait for that whole grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int nw = p.new_len ? min(p.new_len[b], p.M) : p.M;
-  if (m >= nw || *(volatile int*)p.err != 0) return;
-  const int rt = m / p.tok, kvh = h / p.group;
-  const int first = max(p.meta[(b * p.RT + rt) * 2], 0), last = min(p.meta[(b * p.RT + rt) * 2 + 1], p.J - 1);
-  if (first >= last) return;
-  const int U = p.Hkv * p.RT, u = kvh * p.RT + rt;
-  const int r = (m - rt * p.tok) * p.group + h % p.group;
-  // run s: slot 1 of CTA (u, first), slot 0 of the later ones
-  auto row_of = [&](int s) { return (((size_t)s * U + u) * 2 + (s == first ? 1 : 0)) * p.slot_rows + r; };
-  float mx = -INFINITY;
-  for (int s = first + lane; s <= last; s += 32) mx = fmaxf(mx, p.part_ml[row_of(s) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float L = 0.f;
-  float acc[PER];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  if (mx != -INFINITY) {
-    for (int s = first + lane; s <= last; s += 32)
-      L += exp2f(p.part_ml[row_of(s) * 2] - mx) * p.part_ml[row_of(s) * 2 + 1];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-#pragma unroll 4
-    for (int s = first + warp; s <= last; s += CW) {
-      const size_t row = row_of(s);
-      const float w = exp2f(p.part_ml[row * 2] - mx);
-      alignas(16) float v[PER];
-      if constexpr (PER == 4)
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p.part_o + row * HD + lane * PER);
-      else
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p.part_o + row * HD + lane * PER);
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+  if (*(volatile int*)p.err != 0) return;   // the same for the whole grid: nothing sets it now
+  const long long row0 = (long long)blockIdx.x * rpb;
+  float mx, L;
+  Acc<HD> acc;
+  bool many = false;
+  if (warp < rpb) {
+    const Row x = combine_row(p, row0 + warp);
+    many = x.mine && x.last - x.first >= kFewRuns;
+    if (x.mine && !many) {
+      combine_runs<HD>(p, x, 0, 1, lane, mx, L, acc);
+      combine_store<HD, FP16>(p, x, lane, mx, L, acc);
     }
   }
+  if (!__syncthreads_or(many)) return;
+  for (int i = 0; i < rpb; ++i) {
+    const Row x = combine_row(p, row0 + i);
+    if (!x.mine || x.last - x.first < kFewRuns) continue;
+    combine_runs<HD>(p, x, warp, CW, lane, mx, L, acc);
 #pragma unroll
-  for (int e = 0; e < PER; ++e) part[warp][lane * PER + e] = acc[e];
-  __syncthreads();
-  const float inv = mx == -INFINITY ? 0.f : 1.0f / L;
-  const size_t orow = ((size_t)b * p.M + m) * p.H + h;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + orow * HD);
-  for (int c = threadIdx.x; c < HD / 2; c += CW * 32) {
-    float x = 0.f, y = 0.f;
+    for (int e = 0; e < PER; ++e) part[warp][lane * PER + e] = acc.v[e];
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-    for (int w = 0; w < CW; ++w) {
-      x += part[w][2 * c];
-      y += part[w][2 * c + 1];
+      for (int e = 0; e < PER; ++e) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < CW; ++w) s += part[w][lane * PER + e];
+        acc.v[e] = s;
+      }
+      combine_store<HD, FP16>(p, x, lane, mx, L, acc);
     }
-    dst[c] = pack16<FP16>(x * inv, y * inv);
+    __syncthreads();
   }
-  if (threadIdx.x == 0)
-    p.lse[((size_t)b * p.H + h) * p.M + m] = mx == -INFINITY ? -INFINITY : (mx + log2f(L)) * 0.69314718055994531f;
 }
 
 template <int HD, bool FP16>
@@ -775,7 +841,10 @@ cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess || p.J == 1) return e;   // one run: every sequence was written whole
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((long long)p.B * p.M * p.H));
+  // enough rows for several blocks an SM: a row to each warp; else a block to each row
+  const long long rows = (long long)p.B * p.M * p.H;
+  const int rpb = rows >= 8 * kTreeSlots ? CW : 1;
+  cfg.gridDim = dim3((unsigned)((rows + rpb - 1) / rpb));
   cfg.blockDim = dim3(CW * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -783,7 +852,7 @@ cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, FP16>, p);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, FP16>, p, rpb);
 }
 
 }  // namespace tree
