@@ -281,8 +281,8 @@ int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, i
  * a token does not reach it, whatever it holds (infinities and NaN included).
  * dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to dtype for the
  * second product.  Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024
- * (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte aligned, at least
- * s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the GPU
+ * and B * table_width * page_size < 2^35 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
+ * aligned, at least s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the GPU
  * need one each.  Lengths are read on the device only, so a captured call follows them.  Runs
  * up to two kernels on `stream`.  The result does not depend on what else runs.
  */

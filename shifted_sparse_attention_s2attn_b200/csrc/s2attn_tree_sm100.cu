@@ -52,6 +52,7 @@ constexpr int WARP_K = 4, WARP_V = 5, WARP_MMA = 6;
 constexpr uint32_t QBOX = BM * 128;          // 128 rows x 128 B (64 columns)
 constexpr uint32_t KBOX = BN * 128;
 constexpr int NBARS = 2 + 2 * KST + 2 * VST + 2 + 2 + 5;
+constexpr int kSeqCost = 3;                  // of a sequence's end, in key tiles
 constexpr uint32_t TM_COLS = 256;
 constexpr uint32_t TM_O = 128;               // S buffers at columns 0 and 64
 
@@ -71,7 +72,7 @@ struct Cfg {
 struct Params {
   void* o;
   float* lse;
-  float* part_o;     // [U * J][2][slot_rows][HD]
+  float* part_o;     // [U * J][2][HD/4][slot_rows][4]: neighbouring rows' pieces side by side
   float* part_ml;    // [U * J][2][slot_rows][2]
   int* meta;         // [B * RT][2]: first and last run of a sequence
   const int* len;
@@ -97,6 +98,12 @@ __device__ __forceinline__ int cap_tokens(const Params& p) {
 __device__ __forceinline__ int cache_tiles(int len) { return (int)(((long long)len + BN - 1) / BN); }
 __device__ __forceinline__ int all_tiles(int len, int nw, int first_tok) {
   return nw > first_tok ? cache_tiles(len) + (nw + BN - 1) / BN : 0;
+}
+
+// Keys of tile t of a sequence.
+__device__ __forceinline__ int tile_keys(int t, int len, int nw) {
+  const int ct = cache_tiles(len);
+  return t < ct ? min(BN, len - t * BN) : min(BN, nw - (t - ct) * BN);
 }
 
 // Walks the segments of a run: `b` and its tiles [t0, t0 + n) of `total`.
@@ -130,6 +137,25 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, gerr));
 }
 
+__device__ __forceinline__ bool wait_spin_warp(uint64_t* bar, uint32_t parity, volatile int* abort, const int* gerr) {
+  return __all_sync(0xffffffffu, wait_spin(bar, parity, abort, gerr));
+}
+// Columns [4 * piece, 4 * piece + 4) of row r of a partial.
+template <int HD>
+__device__ __forceinline__ float4* part_at(const Params& p, size_t slot, int piece, int r) {
+  return reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + piece) * p.slot_rows + r;
+}
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(x));
+  return x != 0;
+}
+
 // S[128 x 64] = Q K^T, both K-major.
 template <int HD>
 __device__ __forceinline__ void issue_s(uint32_t d, uint32_t sq, uint32_t sk, uint32_t idesc) {
@@ -140,12 +166,13 @@ __device__ __forceinline__ void issue_s(uint32_t d, uint32_t sq, uint32_t sk, ui
            kk > 0 ? 1u : 0u);
 }
 
-// O[128 x HD] (+)= P V: P from TMEM, V seen MN-major.
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t tp, uint32_t sv, uint32_t idesc, bool first) {
+// O[128 x HD] (+)= P V over the tile's first 16 * ksteps keys: P from TMEM, V seen MN-major.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t tp, uint32_t sv, uint32_t idesc, bool first,
+                                         int ksteps) {
   const uint64_t dv = sdesc_sw128(sv, KBOX, 1024);
 #pragma unroll
   for (int kk = 0; kk < BN / 16; ++kk)
-    mma_ts(d, tp + kk * 8, sdesc_add(dv, kk * 2048), idesc, (first && kk == 0) ? 0u : 1u);
+    if (kk < ksteps) mma_ts(d, tp + kk * 8, sdesc_add(dv, kk * 2048), idesc, (first && kk == 0) ? 0u : 1u);
 }
 
 template <bool FP16>
@@ -199,13 +226,14 @@ __device__ __forceinline__ float p_row(const uint32_t (&sr)[64], uint32_t lo, ui
   return ((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y));
 }
 
-// Clears V rows [keep, 64) of a tile and, with `scan`, the elements of the others that are
-// infinite or NaN, whose rows it notes in bad[2].  Row r of column box x lies at
+// Clears V rows behind the `keep` of a tile that the product reads (it goes in steps of 16) and,
+// with `scan`, the elements of the others that are infinite or NaN, whose rows it notes in bad[2].  Row r of column box x lies at
 // x * KBOX + r * 128 whatever the swizzle, which only permutes 16-byte pieces of the row.
 template <int HD, bool FP16>
 __device__ __forceinline__ void clean_v(uint8_t* v, int keep, bool scan, uint32_t* bad, int tid, int nthreads) {
   const uint32_t exp_mask = FP16 ? 0x7c00u : 0x7f80u;
-  for (int i = tid; i < BN * (HD / 8); i += nthreads) {
+  const int rows = (keep + 15) & ~15;
+  for (int i = tid; i < rows * (HD / 8); i += nthreads) {
     const int c = i % (HD / 8), r = i / (HD / 8);   // c: 16-byte piece of the row
     uint4* at = reinterpret_cast<uint4*>(v + (c / 8) * KBOX + r * 128 + (c % 8) * 16);
     if (r >= keep) {
@@ -267,6 +295,15 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     if (threadIdx.x == 0) report_error(p.err, (K_TREE << 8) | SITE_ALIGN);
     return;
   }
+  if (warp == WARP_K && lane == 0) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tkp);
+    prefetch_tmap(&tkn);
+  }
+  if (warp == WARP_V && lane == 0) {
+    prefetch_tmap(&tvp);
+    prefetch_tmap(&tvn);
+  }
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -309,43 +346,55 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (warp == 0) {
-    // this CTA's run: tiles [w0, w1) of the unit's concatenation
-    long long sum = 0;
-    for (int b = lane; b < p.B; b += 32) sum += all_tiles(s_len[b], s_new[b], first_tok);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int runs = (int)min((long long)p.J, max(1LL, sum >> kTreeMinRunLog2));
-    long long w0 = 0, w1 = 0;
-    if (j < runs) {   // the first sum % runs runs have one tile more
-      const long long each = sum <= 0x7fffffff ? (int)sum / runs : sum / runs, more = sum - each * runs;
-      w0 = each * j + min((long long)j, more);
-      w1 = w0 + each + (j < more ? 1 : 0);
+    // This CTA's run.  A sequence weighs its tiles and kSeqCost more: what its end costs (masked
+    // tiles, the output, the next Q).  The run takes the tiles of an equal share of the weights.
+    int sum = 0, weight = 0;       // the host has checked that these fit
+    for (int b = lane; b < p.B; b += 32) {
+      const int n = all_tiles(s_len[b], s_new[b], first_tok);
+      sum += n;
+      weight += n ? n + kSeqCost : 0;
     }
-    // the sequence that holds tile w0
-    int b0 = 0, t0 = 0;
-    long long before = 0;
-    for (int base = 0; base < p.B && w1 > w0; base += 32) {
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    weight = __reduce_add_sync(0xffffffffu, weight);
+    const int runs = min(p.J, max(1, sum >> kTreeMinRunLog2));
+    const int each = weight / runs, more = weight - each * runs;   // the first `more` shares are one larger
+    const int w0 = each * j + min(j, more), w1 = w0 + each + (j < more ? 1 : 0);
+    // the sequence and tile that w0 falls on, and the tiles before w0 and w1
+    int b0 = 0, t0 = 0, at0 = -1, at1 = -1, tiles_before = 0, weight_before = 0;
+    for (int base = 0; base < p.B && j < runs; base += 32) {
       const int b = base + lane;
-      const long long mine = b < p.B ? all_tiles(s_len[b], s_new[b], first_tok) : 0;
-      long long incl = mine;
+      const int n = b < p.B ? all_tiles(s_len[b], s_new[b], first_tok) : 0;
+      int ti = n, wi = n ? n + kSeqCost : 0;      // inclusive sums over the lanes
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int x = __shfl_up_sync(0xffffffffu, ti, o), y = __shfl_up_sync(0xffffffffu, wi, o);
+        if (lane >= o) ti += x, wi += y;
       }
-      const unsigned past = __ballot_sync(0xffffffffu, before + incl > w0);
-      if (past) {
-        const int f = __ffs(past) - 1;
+      const int ws = weight_before + wi - (n ? n + kSeqCost : 0), ts = tiles_before + ti - n;
+      const unsigned h0 = __ballot_sync(0xffffffffu, weight_before + wi > w0);
+      if (at0 < 0 && h0) {
+        const int f = __ffs(h0) - 1;
+        const int tile = min(n, w0 - ws);         // in lane f; n: the sequence's end
         b0 = base + f;
-        t0 = (int)(w0 - before - __shfl_sync(0xffffffffu, incl - mine, f));
+        t0 = __shfl_sync(0xffffffffu, tile, f);
+        at0 = __shfl_sync(0xffffffffu, ts + tile, f);
+        if (t0 == __shfl_sync(0xffffffffu, n, f)) t0 = 0, ++b0;
+      }
+      const unsigned h1 = __ballot_sync(0xffffffffu, weight_before + wi > w1);
+      if (h1) {
+        const int f = __ffs(h1) - 1;
+        at1 = __shfl_sync(0xffffffffu, ts + min(n, w1 - ws), f);
         break;
       }
-      before += __shfl_sync(0xffffffffu, incl, 31);
+      weight_before += __shfl_sync(0xffffffffu, wi, 31);
+      tiles_before += __shfl_sync(0xffffffffu, ti, 31);
     }
+    if (at0 < 0) at0 = sum;      // no tile is left for this run
+    if (at1 < 0) at1 = sum;
     if (lane == 0) {
       run[0] = b0;
       run[1] = t0;
-      run[2] = (int)(w1 - w0);
+      run[2] = j < runs ? at1 - at0 : 0;
       run[3] = runs;
     }
   }
@@ -367,11 +416,6 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     static_assert(KST == VST, "one ring depth");
     const int box_keys = min(1 << p.page_shift, BN);
     const int new_box = min(p.M, BN);
-    if (lane == 0) {
-      if (is_k) prefetch_tmap(&tq);
-      prefetch_tmap(mp);
-      prefetch_tmap(mn);
-    }
     bool ok = true;
     int i = 0, n_seg = 0;
     while (ok && seg.next()) {
@@ -440,59 +484,71 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     }
     __syncwarp();
   } else if (!skip && warp == WARP_MMA) {
-    if (lane == 0) {
-      // ---------------- MMA issuer: S(i) | P(i-1) V(i-1) ----------------
-      const uint32_t fmt = FP16 ? ~((1u << 7) | (1u << 10)) : ~0u;   // A and B formats: 0 = f16, 1 = bf16
-      const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false) & fmt;
-      const uint32_t id_pv = idesc_bf16_f32(BM, HD, false, true) & fmt;
-      const uint32_t sq = smem_u32(smem), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
-      bool ok = true;
-      int ns = 0, np = 0;             // segments whose S, whose first PV was issued
-      int s_left = 0, pv_left = 0;    // tiles left in the segment of S and of PV
-      Segments sp(s_len, s_new, first_tok, run[0], run[1], n_tiles);
-      for (int i = 0; i <= n_tiles && ok; ++i) {
-        if (i < n_tiles) {
-          if (s_left == 0) {
-            seg.next();
-            s_left = seg.n;
-            ok = wait_spin(q_full, ns & 1, abort_flag, p.err);
-            ++ns;
-          }
-          if (ok) ok = wait_spin(&k_full[i % KST], (i / KST) & 1, abort_flag, p.err);
-          if (!ok) break;
-          tc_fence_after();
+    // ---------------- MMA issuer: S(i) | P(i-1) V(i-1) ----------------
+    // The whole warp walks the tiles and one elected lane issues: where the compiler sees that
+    // one lane runs, an MMA's operands go straight to uniform registers (P V of a tile: 423 ->
+    // 130 cycles to issue, against `if (lane == 0)`).
+    const uint32_t fmt = FP16 ? ~((1u << 7) | (1u << 10)) : ~0u;   // A and B formats: 0 = f16, 1 = bf16
+    const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false) & fmt;
+    const uint32_t id_pv = idesc_bf16_f32(BM, HD, false, true) & fmt;
+    const uint32_t sq = smem_u32(smem), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
+    bool ok = true;
+    int ns = 0, np = 0;             // segments whose S, whose first PV was issued
+    int s_left = 0, pv_left = 0;    // tiles left in the segment of S and of PV
+    Segments sp(s_len, s_new, first_tok, run[0], run[1], n_tiles);
+    for (int i = 0; i <= n_tiles && ok; ++i) {
+      if (i < n_tiles) {
+        if (s_left == 0) {
+          seg.next();
+          s_left = seg.n;
+          ok = wait_spin_warp(q_full, ns & 1, abort_flag, p.err);
+          ++ns;
+        }
+        if (ok) ok = wait_spin_warp(&k_full[i % KST], (i / KST) & 1, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        --s_left;
+        if (elect_one()) {
           issue_s<HD>(tmem + (uint32_t)BN * (i & 1), sq, sk + (i % KST) * C::KTILE, id_s);
           mma_commit(&s_full[i & 1]);
           mma_commit(&k_empty[i % KST]);
-          if (--s_left == 0) mma_commit(q_empty);
+          if (s_left == 0) mma_commit(q_empty);
         }
-        if (i > 0) {
-          const int t = i - 1;
-          bool first = false;
-          if (pv_left == 0) {
-            sp.next();
-            pv_left = sp.n;
-            first = true;
-            if (np > 0) ok = wait_spin(o_free, (np - 1) & 1, abort_flag, p.err);   // O of the last segment read
-            ++np;
-          }
-          if (ok) ok = wait_spin(&p_ready[t & 1], (t >> 1) & 1, abort_flag, p.err);
-          if (ok) ok = wait_spin(&v_full[t % VST], (t / VST) & 1, abort_flag, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(tmem + TM_O, tmem + (uint32_t)BN * (t & 1), sv + (t % VST) * C::KTILE, id_pv, first);
+        __syncwarp();
+      }
+      if (i > 0) {
+        const int t = i - 1;
+        bool first = false;
+        if (pv_left == 0) {
+          sp.next();
+          pv_left = sp.n;
+          first = true;
+          if (np > 0) ok = wait_spin_warp(o_free, (np - 1) & 1, abort_flag, p.err);   // O of the last segment read
+          ++np;
+        }
+        if (ok) ok = wait_spin_warp(&p_ready[t & 1], (t >> 1) & 1, abort_flag, p.err);
+        if (ok) ok = wait_spin_warp(&v_full[t % VST], (t / VST) & 1, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+        const int pv_tile = sp.t0 + sp.n - pv_left;
+        --pv_left;
+        if (elect_one()) {
+          issue_pv(tmem + TM_O, tmem + (uint32_t)BN * (t & 1), sv + (t % VST) * C::KTILE, id_pv, first,
+                   (tile_keys(pv_tile, s_len[sp.b], s_new[sp.b]) + 15) / 16);
           mma_commit(pv_done);
           mma_commit(&v_empty[t % VST]);
-          if (--pv_left == 0) mma_commit(o_full);
+          if (pv_left == 0) mma_commit(o_full);
         }
+        __syncwarp();
       }
-      if (!ok) {
-        report_error(p.err, (K_TREE << 8) | SITE_MMA);
-        *abort_flag = 1;
-      }
-      mma_commit(drain);
-      if (!wait_drain(drain, 0)) report_error(p.err, (K_TREE << 8) | SITE_DRAIN);
     }
+    if (!ok && lane == 0) {
+      report_error(p.err, (K_TREE << 8) | SITE_MMA);
+      *abort_flag = 1;
+    }
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
+    if (!wait_drain(drain, 0) && lane == 0) report_error(p.err, (K_TREE << 8) | SITE_DRAIN);
     __syncwarp();
   } else if (!skip && warp < n_act) {
     // ---------------- softmax: thread = query row ----------------
@@ -508,27 +564,30 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       const int b = seg.b, len = s_len[b], nw = s_new[b], ct = cache_tiles(len);
       const bool row_ok = in_tile && m < nw;
       uint32_t* bad_rows = bad + 4 * (n_draft % 3);        // of this sequence's drafted tiles
+      const bool has_draft = seg.t0 + seg.n > ct;
+      // which drafted keys the row sees
+      unsigned long long see[2] = {0, 0};
+      if (has_draft && row_ok) {
+        if (p.mask) {
+          const unsigned long long* w = p.mask + ((size_t)b * p.M + m) * p.words;
+          see[0] = w[0];
+          if (p.words > 1) see[1] = w[1];
+        } else {     // j <= m
+          see[0] = m >= 63 ? ~0ull : (2ull << m) - 1ull;
+          see[1] = m < 64 ? 0ull : m >= 127 ? ~0ull : (2ull << (m - 64)) - 1ull;
+        }
+      }
       float m_run = -INFINITY, l_run = 0.f;
       for (int t = seg.t0; t < seg.t0 + seg.n && ok; ++t, ++i) {
         const int buf = i & 1;
         // keys of the tile, and which of them the row sees
         const bool draft = t >= ct;
-        const int keep = draft ? min(BN, nw - (t - ct) * BN) : min(BN, len - t * BN);
+        const int keep = tile_keys(t, len, nw);
         const bool edge = draft || keep < BN;
         uint32_t lo = 0xffffffffu, hi = 0xffffffffu;
         if (edge) {
           unsigned long long vis = keep >= 64 ? ~0ull : (1ull << keep) - 1ull;
-          if (draft) {
-            const int d = t - ct;
-            if (!row_ok) {
-              vis = 0;
-            } else if (p.mask) {
-              vis &= p.mask[((size_t)b * p.M + m) * p.words + d];
-            } else {
-              const int last = m - d * BN;                 // j <= m
-              vis &= last >= 63 ? ~0ull : last < 0 ? 0ull : (2ull << last) - 1ull;
-            }
-          }
+          if (draft) vis &= t == ct ? see[0] : see[1];
           lo = (uint32_t)vis;
           hi = (uint32_t)(vis >> 32);
           ok = wait_warp(&v_full[i % VST], (i / VST) & 1, abort_flag, p.err);
@@ -591,7 +650,6 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       if (ok) ok = wait_warp(o_full, n_seg & 1, abort_flag, p.err);
       if (!ok) break;
       tc_fence_after();
-      const bool has_draft = seg.t0 + seg.n > ct;
       uint32_t fix[4] = {0, 0, 0, 0};      // drafted rows with inf/NaN that this row sees
       if (has_draft) {
         // every warp has noted its rows; the notes of the sequence after the next start from
@@ -601,22 +659,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         if (!ok) break;
         if (threadIdx.x < 4) bad[4 * ((n_draft + 2) % 3) + threadIdx.x] = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          fix[e] = row_ok ? bad_rows[e] : 0u;
-          if (fix[e] == 0) continue;
-          uint32_t see;
-          if (p.mask) {
-            see = e / 2 < p.words ? (uint32_t)(p.mask[((size_t)b * p.M + m) * p.words + e / 2] >> (32 * (e % 2))) : 0u;
-          } else {
-            const int last = m - e * 32;
-            see = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
-          }
-          fix[e] &= see;
-        }
+        for (int e = 0; e < 4; ++e) fix[e] = bad_rows[e] & (uint32_t)(see[e / 2] >> (32 * (e % 2)));
         ++n_draft;
       }
       const bool whole = seg.t0 == 0 && seg.n == seg.total;
-      const size_t part = ((size_t)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0)) * p.slot_rows + r;
+      const size_t slot = (size_t)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0), part = slot * p.slot_rows + r;
       const size_t orow = ((size_t)b * p.M + m) * p.H + h;
       const bool st_ok =
           row_ok && (whole ? in_bounds(orow, 1, (size_t)p.B * p.M * p.H, p.err, (K_TREE << 8) | SITE_STORE)
@@ -639,10 +686,10 @@ __global__ void __launch_bounds__(NTHREADS, 2)
             dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else if (st_ok) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part * HD + c);
+          float4* dst = part_at<HD>(p, slot, c / 4, r);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            dst[x] = make_float4(__uint_as_float(rr[4 * x]), __uint_as_float(rr[4 * x + 1]),
+            dst[(size_t)x * p.slot_rows] = make_float4(__uint_as_float(rr[4 * x]), __uint_as_float(rr[4 * x + 1]),
                                  __uint_as_float(rr[4 * x + 2]), __uint_as_float(rr[4 * x + 3]));
         }
       }
@@ -661,7 +708,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
               uint16_t* at = static_cast<uint16_t*>(p.o) + orow * HD + c;
               *at = (uint16_t)pack16<FP16>(unpack16<FP16>(*at) + f, 0.f);
             } else {
-              p.part_o[part * HD + c] += f;
+              reinterpret_cast<float*>(part_at<HD>(p, slot, c / 4, r))[c % 4] += f;
             }
           }
         }
@@ -671,7 +718,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           p.lse[((size_t)b * p.H + h) * p.M + m] =
               l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
         } else {
-          p.part_ml[part * 2] = m_run;
+          // a row all of whose scores were NaN has no maximum: 0 takes its NaN sum through the join
+          p.part_ml[part * 2] = l_run != l_run && m_run == -INFINITY ? 0.f : m_run;
           p.part_ml[part * 2 + 1] = l_run;
         }
       }
@@ -700,126 +748,88 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 
 // o = sum_s 2^(m_s - mx) o_s / sum_s 2^(m_s - mx) l_s over the runs s of the row's sequence;
 // lse = ln2 * (mx + log2 L).  Rows of a sequence that lay in one run were written by the run.
-// A block takes `rpb` rows: each of its warps one row if the row has few runs, all of them one
-// row after another if it has many (a run's row is 512 B: a warp's lanes take 16 B each).
+// A lane joins four columns of one row: block (sequence, unit, 32 rows, 8 / ws pieces of four
+// columns).  The runs of a row are dealt to `ws` warps and, where fewer than 32 rows exist, to
+// the lanes left over; each keeps a running (max, sum, output) and these are joined at the end.
 constexpr int CW = 8;
-constexpr int kFewRuns = 16;
 
-struct Row {
-  int b, m, h, first, last, u, r;
-  bool mine;    // the row has partials
+struct Joined {
+  float mx, L;
+  float4 o;
 };
-__device__ __forceinline__ Row combine_row(const Params& p, long long i) {
-  Row x{};
-  if (i >= (long long)p.B * p.M * p.H) return x;
-  x.h = (int)(i % p.H);
-  x.m = (int)(i / p.H % p.M);
-  x.b = (int)(i / ((long long)p.H * p.M));
-  const int nw = p.new_len ? min(p.new_len[x.b], p.M) : p.M;
-  if (x.m >= nw) return x;
-  const int rt = x.m / p.tok, kvh = x.h / p.group;
-  x.first = max(p.meta[(x.b * p.RT + rt) * 2], 0);
-  x.last = min(p.meta[(x.b * p.RT + rt) * 2 + 1], p.J - 1);
-  x.u = kvh * p.RT + rt;
-  x.r = (x.m - rt * p.tok) * p.group + x.h % p.group;
-  x.mine = x.first < x.last;
-  return x;
-}
-
-template <int HD>
-struct Acc {
-  static constexpr int PER = HD / 32;
-  float v[PER];
-};
-
-// Runs first + from, first + from + step, ... of a row: max over all runs in mx, their sum in L.
-template <int HD>
-__device__ __forceinline__ void combine_runs(const Params& p, const Row& x, int from, int step, int lane, float& mx,
-                                             float& L, Acc<HD>& acc) {
-  constexpr int PER = HD / 32;
-  const int U = p.Hkv * p.RT;
-  // run s: slot 1 of CTA (u, first), slot 0 of the later ones
-  auto row_of = [&](int s) { return (((size_t)s * U + x.u) * 2 + (s == x.first ? 1 : 0)) * p.slot_rows + x.r; };
-  mx = -INFINITY;
-  for (int s = x.first + lane; s <= x.last; s += 32) mx = fmaxf(mx, p.part_ml[row_of(s) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  L = 0.f;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc.v[e] = 0.f;
-  if (mx == -INFINITY) return;
-  for (int s = x.first + lane; s <= x.last; s += 32)
-    L += exp2f(p.part_ml[row_of(s) * 2] - mx) * p.part_ml[row_of(s) * 2 + 1];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-#pragma unroll 4
-  for (int s = x.first + from; s <= x.last; s += step) {
-    const size_t row = row_of(s);
-    const float w = exp2f(p.part_ml[row * 2] - mx);
-    alignas(16) float v[PER];
-    if constexpr (PER == 4)
-      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p.part_o + row * HD + lane * PER);
-    else
-      *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p.part_o + row * HD + lane * PER);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc.v[e] = fmaf(w, v[e], acc.v[e]);
-  }
+__device__ __forceinline__ void join(Joined& a, float mx, float L, const float4& o) {
+  const float top = fmaxf(a.mx, mx);
+  if (top == -INFINITY) return;                 // neither has seen a key
+  const float x = ex2_approx(a.mx - top), y = ex2_approx(mx - top);
+  a.mx = top;
+  a.L = fmaf(a.L, x, L * y);
+  a.o = make_float4(fmaf(a.o.x, x, o.x * y), fmaf(a.o.y, x, o.y * y), fmaf(a.o.z, x, o.z * y), fmaf(a.o.w, x, o.w * y));
 }
 
 template <int HD, bool FP16>
-__device__ __forceinline__ void combine_store(const Params& p, const Row& x, int lane, float mx, float L,
-                                              const Acc<HD>& acc) {
-  constexpr int PER = HD / 32;
-  const float inv = mx == -INFINITY ? 0.f : 1.0f / L;
-  const size_t orow = ((size_t)x.b * p.M + x.m) * p.H + x.h;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + orow * HD) + lane * (PER / 2);
-#pragma unroll
-  for (int e = 0; e < PER / 2; ++e) dst[e] = pack16<FP16>(acc.v[2 * e] * inv, acc.v[2 * e + 1] * inv);
-  if (lane == 0)
-    p.lse[((size_t)x.b * p.H + x.h) * p.M + x.m] =
-        mx == -INFINITY ? -INFINITY : (mx + log2f(L)) * 0.69314718055994531f;
-}
-
-template <int HD, bool FP16>
-__global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_constant__ Params p, int rpb) {
-  constexpr int PER = HD / 32;
-  __shared__ float part[CW][HD];
+__global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_constant__ Params p, int ws, int rp) {
+  __shared__ Joined part[CW][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int wc = CW / ws;                                 // pieces of a block
+  const int piece = (int)blockIdx.y * wc + warp / ws, split = warp % ws;
+  const int groups = (p.slot_rows + rp - 1) / rp, U = p.Hkv * p.RT;
+  const int grp = (int)blockIdx.x % groups, u = (int)blockIdx.x / groups % U, b = (int)blockIdx.x / (groups * U);
+  const int kvh = u / p.RT, rt = u % p.RT;
+  const int r = grp * rp + lane % rp, sub = lane / rp, parts = ws * (32 / rp);
+  const int m = rt * p.tok + r / p.group, h = kvh * p.group + r % p.group;
   // launched as a programmatic dependent of the attention kernel: wait for that whole grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (*(volatile int*)p.err != 0) return;   // the same for the whole grid: nothing sets it now
-  const long long row0 = (long long)blockIdx.x * rpb;
-  float mx, L;
-  Acc<HD> acc;
-  bool many = false;
-  if (warp < rpb) {
-    const Row x = combine_row(p, row0 + warp);
-    many = x.mine && x.last - x.first >= kFewRuns;
-    if (x.mine && !many) {
-      combine_runs<HD>(p, x, 0, 1, lane, mx, L, acc);
-      combine_store<HD, FP16>(p, x, lane, mx, L, acc);
+  const int nw = p.new_len ? min(p.new_len[b], p.M) : p.M;
+  if (nw <= rt * p.tok || *(volatile int*)p.err != 0) return;   // the same for the whole block
+  const int2 fl = *reinterpret_cast<const int2*>(p.meta + (b * p.RT + rt) * 2);
+  const int first = max(fl.x, 0), last = min(fl.y, p.J - 1);
+  if (first >= last) return;
+  const bool live = r < p.slot_rows && m < nw;
+  Joined a = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  // run s: slot 1 of CTA (u, first), slot 0 of the later ones
+  constexpr int AHEAD = 4;
+  for (int s0 = first + split * (32 / rp) + sub; s0 <= last && live; s0 += AHEAD * parts) {
+    float2 ml[AHEAD];
+    float4 v[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int s = s0 + k * parts;
+      ml[k] = make_float2(-INFINITY, 0.f);
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s > last) continue;
+      const size_t slot = ((size_t)s * U + u) * 2 + (s == first ? 1 : 0);
+      ml[k] = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.slot_rows + r) * 2);
+      v[k] = *part_at<HD>(p, slot, piece, r);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) join(a, ml[k].x, ml[k].y, v[k]);
+  }
+  __syncwarp();
+  for (int o = rp; o < 32; o <<= 1) {     // the lanes that hold the same row
+    Joined x;
+    x.mx = __shfl_xor_sync(0xffffffffu, a.mx, o);
+    x.L = __shfl_xor_sync(0xffffffffu, a.L, o);
+    x.o = make_float4(__shfl_xor_sync(0xffffffffu, a.o.x, o), __shfl_xor_sync(0xffffffffu, a.o.y, o),
+                      __shfl_xor_sync(0xffffffffu, a.o.z, o), __shfl_xor_sync(0xffffffffu, a.o.w, o));
+    join(a, x.mx, x.L, x.o);
+  }
+  if (ws > 1) {
+    part[warp][lane] = a;
+    __syncthreads();
+    if (split) return;
+    for (int w = 1; w < ws; ++w) {
+      const Joined& x = part[warp + w][lane];
+      join(a, x.mx, x.L, x.o);
     }
   }
-  if (!__syncthreads_or(many)) return;
-  for (int i = 0; i < rpb; ++i) {
-    const Row x = combine_row(p, row0 + i);
-    if (!x.mine || x.last - x.first < kFewRuns) continue;
-    combine_runs<HD>(p, x, warp, CW, lane, mx, L, acc);
-#pragma unroll
-    for (int e = 0; e < PER; ++e) part[warp][lane * PER + e] = acc.v[e];
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < CW; ++w) s += part[w][lane * PER + e];
-        acc.v[e] = s;
-      }
-      combine_store<HD, FP16>(p, x, lane, mx, L, acc);
-    }
-    __syncthreads();
-  }
+  if (!live || sub) return;
+  const float inv = a.mx == -INFINITY ? 0.f : 1.0f / a.L;
+  const size_t orow = ((size_t)b * p.M + m) * p.H + h;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + orow * HD + 4 * piece) =
+      make_uint2(pack16<FP16>(a.o.x * inv, a.o.y * inv), pack16<FP16>(a.o.z * inv, a.o.w * inv));
+  if (piece == 0)
+    p.lse[((size_t)b * p.H + h) * p.M + m] =
+        a.mx == -INFINITY ? -INFINITY : (a.mx + log2f(a.L)) * 0.69314718055994531f;
 }
 
 template <int HD, bool FP16>
@@ -841,10 +851,12 @@ cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess || p.J == 1) return e;   // one run: every sequence was written whole
   cudaLaunchConfig_t cfg = {};
-  // enough rows for several blocks an SM: a row to each warp; else a block to each row
-  const long long rows = (long long)p.B * p.M * p.H;
-  const int rpb = rows >= 8 * kTreeSlots ? CW : 1;
-  cfg.gridDim = dim3((unsigned)((rows + rpb - 1) / rpb));
+  // a sequence has about J / B runs: with many, four warps share a row's
+  const int ws = p.J >= 16 * p.B ? 4 : 1;
+  int rp = 1;
+  while (rp < 32 && rp < p.slot_rows) rp *= 2;
+  const long long blocks = (long long)p.B * p.Hkv * p.RT * ((p.slot_rows + rp - 1) / rp);
+  cfg.gridDim = dim3((unsigned)blocks, HD / 4 / (CW / ws));
   cfg.blockDim = dim3(CW * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -852,7 +864,7 @@ cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, FP16>, p, rpb);
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, FP16>, p, ws, rp);
 }
 
 }  // namespace tree

@@ -127,7 +127,7 @@ def _tree(lib, ptrs=None, B=2, M=4, H=8, Hkv=2, D=128, n_pages=10, page=16, widt
 
 @pytest.mark.parametrize("bad,status", [
     (dict(B=0), -1), (dict(M=0), -1), (dict(H=7), -1), (dict(Hkv=0), -1), (dict(dtype=2), -1), (dict(n_pages=0), -1),
-    (dict(width=0), -1), (dict(B=1025), -2), (dict(M=129), -2), (dict(D=96), -2), (dict(D=256), -2),
+    (dict(width=0), -1), (dict(width=1 << 30, B=600), -2), (dict(B=1025), -2), (dict(M=129), -2), (dict(D=96), -2), (dict(D=256), -2),
     (dict(H=129, Hkv=1), -2), (dict(page=24), -2), (dict(page=8), -2), (dict(n_pages=1 << 27, page=16), -2),
     (dict(ws=NULL), -3), (dict(ws=P + 64), -3), (dict(n=100), -3),
     (dict(ptrs=dict(q=NULL)), -1), (dict(ptrs=dict(vp=P + 8)), -1), (dict(ptrs=dict(len=NULL)), -1),
