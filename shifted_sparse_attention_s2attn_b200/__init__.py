@@ -79,7 +79,7 @@ def capi():
         "s2attn_tree_decode_workspace_bytes": ([I, I, I, I, I], Z),
         "s2attn_tree_decode": ([P] * 11 + [I] * 9 + [P, Z, P], I),
         "s2attn_cache_append": ([P] * 8 + [I] * 9 + [P], I),
-        "s2attn_cache_copy_pages": ([ctypes.POINTER(P), I, ctypes.POINTER(I), I, I, Z, P], I),
+        "s2attn_cache_copy_pages": ([P, I, P, I, I, Z, P], I),
         "s2attn_get_device_error": ([ctypes.POINTER(I)], I),
         "s2attn_clear_device_error": ([], I),
         "s2attn_selftest_bounded_wait": ([ctypes.c_uint, P], I),
@@ -652,7 +652,9 @@ def s2attn_cache_copy_pages(pools, pairs, stream=None):
     if len(shape) < 2:
         raise ValueError("a pool must be [n_pages, ...]")
     for t in pools:
-        _fit(t, "every pool", shape, dtype, dev)
+        if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+            _fit(t, "every pool", shape, dtype, dev)
+    addresses = array.array("Q", [t.data_ptr() for t in pools])
     flat = array.array("i", bytes(8 * len(pairs)))
     if len(pairs):
         src, dst = zip(*pairs, strict=True)      # a pair of any other length raises ValueError
@@ -661,8 +663,8 @@ def s2attn_cache_copy_pages(pools, pairs, stream=None):
         except OverflowError:
             raise ValueError("a page number does not fit 32 bits") from None
     n_pages = shape[0]
-    _call_on(dev, "s2attn_cache_copy_pages", stream, _ptr_array(pools), len(pools),
-             (ctypes.c_int * len(flat)).from_buffer(flat) if len(flat) else None, len(pairs), n_pages,
+    _call_on(dev, "s2attn_cache_copy_pages", stream, addresses.buffer_info()[0], len(pools), flat.buffer_info()[0],
+             len(pairs), n_pages,
              ref.numel() // max(n_pages, 1) * ref.element_size())
 
 

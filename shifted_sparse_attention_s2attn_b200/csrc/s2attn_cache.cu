@@ -3,6 +3,8 @@
 //
 // The copies are HBM-bound: each byte is read once and written once.  A thread moves four
 // 16-byte pieces and has all four loads in flight before the first store.
+#include <algorithm>
+
 #include "s2_internal.h"
 #include "s2_ptx.cuh"
 
@@ -11,10 +13,11 @@ namespace cache {
 
 constexpr int THREADS = 256;
 constexpr int UNROLL = 4;
+constexpr int MAX_SLOTS = 256;   // of a block of the append kernel
 
 struct AppendArgs {
-  const uint4* src[2];       // k_new, v_new [B, M, Hkv, D]
-  uint4* dst[2];             // k_pages, v_pages [n_pages, page_size, Hkv, D]
+  const uint4 *k_new, *v_new;  // [B, M, Hkv, D]
+  uint4 *k_pages, *v_pages;  // [n_pages, page_size, Hkv, D]
   const int* table;          // [B, width]
   const int* len;            // [B]
   const int* rows;           // [B, A] or NULL: row j is new row j
@@ -25,45 +28,54 @@ struct AppendArgs {
   int* index_err;
 };
 
-// blockIdx.y: K or V.  Slot t = (b, j); a row outside the new rows, a position outside the
-// table or a page outside the pool is recorded and skipped.
+// Slot t = (b, j) of a block's `tpb`: its rows of k_new and v_new are found by one thread (a row
+// outside the new rows, a position outside the table or a page outside the pool is recorded
+// and skipped), then all threads copy the slots' rows.
 __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendArgs a) {
-  const uint4* src = a.src[blockIdx.y];
-  uint4* dst = a.dst[blockIdx.y];
+  __shared__ long long s_src[MAX_SLOTS], s_dst[MAX_SLOTS];   // first piece of the row; -1: no row
   const long long slot0 = (long long)blockIdx.x * a.tpb;
-  const long long slots = (long long)a.B * a.A;
-  const int n = (int)min((long long)a.tpb, slots - slot0) * a.cpr;
+  const int slots = (int)min((long long)a.tpb, (long long)a.B * a.A - slot0);
+  for (int i = threadIdx.x; i < slots; i += THREADS) {
+    const long long slot = slot0 + i;
+    const int b = (int)(slot / a.A), j = (int)(slot - (long long)b * a.A);
+    long long src = -1, dst = -1;
+    if (!a.n_rows || j < a.n_rows[b]) {
+      const int row = a.rows ? a.rows[slot] : j;
+      const long long pos = (long long)a.len[b] + j, pg = pos >> a.page_shift;
+      int page = -1;
+      if (row >= 0 && row < a.M && pos >= 0 && pg < a.width) page = a.table[(size_t)b * a.width + pg];
+      if (page >= 0 && page < a.n_pages) {
+        src = ((long long)b * a.M + row) * a.cpr;
+        dst = (((long long)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * a.cpr;
+      } else {
+        report_error(a.index_err, (K_CACHE << 8) | SITE_INDEX);
+      }
+    }
+    s_src[i] = src;
+    s_dst[i] = dst;
+  }
+  __syncthreads();
+  const int n = slots * a.cpr;
   for (int i0 = threadIdx.x; i0 < n; i0 += THREADS * UNROLL) {
-    uint4 v[UNROLL];
+    uint4 k[UNROLL], v[UNROLL];
     long long to[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int i = i0 + u * THREADS;
       to[u] = -1;
       if (i >= n) continue;
-      const int c = i % a.cpr;
-      const long long slot = slot0 + i / a.cpr;
-      const int b = (int)(slot / a.A), j = (int)(slot % a.A);
-      if (a.n_rows && j >= a.n_rows[b]) continue;
-      const int row = a.rows ? a.rows[(size_t)b * a.A + j] : j;
-      const long long pos = (long long)a.len[b] + j;
-      const long long pg = pos >> a.page_shift;
-      if (row < 0 || row >= a.M || pos < 0 || pg >= a.width) {
-        report_error(a.index_err, (K_CACHE << 8) | SITE_INDEX);
-        continue;
-      }
-      const int page = a.table[(size_t)b * a.width + pg];
-      if (page < 0 || page >= a.n_pages) {
-        report_error(a.index_err, (K_CACHE << 8) | SITE_INDEX);
-        continue;
-      }
-      const long long in_page = pos & ((1 << a.page_shift) - 1);
-      to[u] = ((((long long)page << a.page_shift) + in_page) * a.cpr) + c;
-      v[u] = src[((long long)b * a.M + row) * a.cpr + c];
+      const int s = i / a.cpr, c = i - s * a.cpr;
+      if (s_dst[s] < 0) continue;
+      to[u] = s_dst[s] + c;
+      k[u] = a.k_new[s_src[s] + c];
+      v[u] = a.v_new[s_src[s] + c];
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u)
-      if (to[u] >= 0) dst[to[u]] = v[u];
+      if (to[u] >= 0) {
+        a.k_pages[to[u]] = k[u];
+        a.v_pages[to[u]] = v[u];
+      }
   }
 }
 
@@ -131,16 +143,18 @@ cudaError_t launch_cache_append(const void* k_new, const void* v_new, void* k_pa
                                 const int* len, const int* rows, const int* n_rows, int B, int M, int A, int width,
                                 int n_pages, int page_shift, int row_bytes, int* index_err, cudaStream_t st) {
   cache::AppendArgs a{};
-  a.src[0] = static_cast<const uint4*>(k_new), a.src[1] = static_cast<const uint4*>(v_new);
-  a.dst[0] = static_cast<uint4*>(k_pages), a.dst[1] = static_cast<uint4*>(v_pages);
+  a.k_new = static_cast<const uint4*>(k_new), a.v_new = static_cast<const uint4*>(v_new);
+  a.k_pages = static_cast<uint4*>(k_pages), a.v_pages = static_cast<uint4*>(v_pages);
   a.table = table, a.len = len, a.rows = rows, a.n_rows = n_rows;
   a.B = B, a.M = M, a.A = A, a.width = width, a.n_pages = n_pages, a.page_shift = page_shift;
   a.cpr = row_bytes / 16;
+  // one step of the block's threads, fewer slots where that leaves SMs without a block
   const int per_block = cache::THREADS * cache::UNROLL;
-  a.tpb = a.cpr < per_block ? per_block / a.cpr : 1;
+  const long long slots = (long long)B * A;
+  a.tpb = (int)std::max(1LL, std::min({(long long)per_block / a.cpr, (long long)cache::MAX_SLOTS, slots / 148}));
   a.index_err = index_err;
-  const long long blocks = ((long long)B * A + a.tpb - 1) / a.tpb;
-  cache::append_kernel<<<dim3((unsigned)blocks, 2), cache::THREADS, 0, st>>>(a);
+  const long long blocks = (slots + a.tpb - 1) / a.tpb;
+  cache::append_kernel<<<(unsigned)blocks, cache::THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
