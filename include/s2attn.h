@@ -210,7 +210,7 @@ int rope_pi_apply_offset(void* q, void* k, int B, int N, int H, int D, int pos0,
  * dtype: S2ATTN_BF16, S2ATTN_FP16 or S2ATTN_F32.  Sums and products are fp32, angles are formed
  * and reduced in 64 bits, the result is rounded once.  q_out == q and k_out == k (in place) are
  * allowed; other overlaps are not.  Requirements: D % 16 == 0, D <= 256; R % 16 == 0,
- * 0 <= R <= D; eps >= 0; device pointers 16-byte aligned (positions and inv_freq 4-byte).
+ * 0 <= R <= D; Hq, Hk <= 16384; eps >= 0; device pointers 16-byte aligned (positions and inv_freq 4-byte).
  */
 int qk_norm_rope_fwd(const void* q, const void* k, const void* wq, const void* wk, const int* positions,
                      const float* inv_freq, void* q_out, void* k_out, int B, int N, int Hq, int Hk, int D, int R,

@@ -129,6 +129,7 @@ struct NormRopeArgs {
   int B, N, Hq, Hk, D, R, pos0, interleaved, norm, dtype;
   float eps, attn_factor;
 };
+constexpr int kNormRopeMaxHeads = 16384;
 constexpr int kNormRopePartials = 1024;   // rows of the backward's partial sums, at most
 cudaError_t launch_norm_rope_fwd(const NormRopeArgs& a, int n_sm, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* part, int n_sm, cudaStream_t st);

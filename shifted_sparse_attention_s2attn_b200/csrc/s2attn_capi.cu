@@ -260,7 +260,7 @@ int check_norm_rope(const s2::NormRopeArgs& a, bool bwd) {
       if (src[i] && !bwd) return S2ATTN_ERR_INVALID_ARG;   // an input without its output
       continue;
     }
-    if (H[i] < 1 || H[i] > 65536) return S2ATTN_ERR_INVALID_ARG;
+    if (H[i] < 1 || H[i] > s2::kNormRopeMaxHeads) return S2ATTN_ERR_INVALID_ARG;
     if (!aligned16(dst[i]) || (w[i] && !aligned16(w[i]))) return S2ATTN_ERR_INVALID_ARG;
     if ((!bwd || a.norm) && !aligned16(src[i])) return S2ATTN_ERR_INVALID_ARG;
     if (bwd && !aligned16(grad[i])) return S2ATTN_ERR_INVALID_ARG;

@@ -9,14 +9,14 @@
 //   dx = (gx - xhat * mean(gx * xhat)) / rms,   dw = sum over rows of g * xhat.
 //
 // HBM-bound: the forward moves each element twice, the backward three times, against about
-// ten flops.  So a row is held in the registers of D/16 lanes from its load to its store:
-// a lane takes two chunks of 8 elements that hold both halves of its pairs (chunk c and
-// chunk c + R/16), hence the rotation needs no exchange, and the two sums of the norm are
-// shuffles over the row's lanes.  cos and sin are the same for all heads of a token: a CTA
-// takes a tile of tokens and computes them once into shared memory, so that no table of
-// positions is kept in HBM and any position is served.  The turn t * inv_freq / 2pi is
-// formed and reduced to [-1/2, 1/2] in 64 bits (in 32 a position of 100k would leave 2^-8
-// of a turn's precision), then sincospif runs on the remainder in 32.
+// ten flops.  A row is held in the registers of D/16 lanes from its load to its store: a lane
+// takes two chunks of 8 elements that hold both halves of its pairs (chunk c and chunk
+// c + R/16), hence the rotation needs no exchange, and the two sums of the norm are shuffles
+// over the row's lanes; the next row's loads go out before a row is worked on.  cos and sin
+// are the same for all heads of a token, so a CTA computes them once for a tile of tokens, in
+// shared memory: no table of positions is kept in HBM and any position is served.  The turn
+// t * inv_freq / 2pi is formed and reduced to [-1/2, 1/2] in 64 bits (in 32 a position of 100k
+// would leave 2^-8 of a turn's precision), then sincospif runs on the remainder in 32.
 // All arithmetic is fp32; y, dx and dw are rounded once, at the end.
 // dw: a thread keeps the sums of its 16 columns over all rows it takes, the CTA adds its
 // rows' threads in a fixed order and writes one partial; a second kernel adds the partials
@@ -33,21 +33,19 @@ namespace s2 {
 namespace nr {
 
 constexpr int THREADS = 256;
-constexpr int FWD_CTAS = 6, BWD_CTAS = 4;    // CTAs an SM, at most
-constexpr int MAX_TAB = 4096;   // (cos, sin) pairs a CTA holds: 32 KB
+// CTAs an SM, all resident at once (a 32k prompt, 32 + 32 heads: 3 183 us, 2 215, 4 (64 registers,
+// spills) 201; 8k forward and backward, 32 + 8 heads: backward at 2 90 us, at 3 (spills) 118)
+constexpr int FWD_CTAS = 3, BWD_CTAS = 2;
+constexpr int MAX_TAB = 2048;   // (cos, sin) pairs of a tile, at most: 16 KB
 
 struct Side {                   // q or k
   const void* x;
   const void* dy;               // backward only
   void* y;                      // forward: the output; backward: dx
   const void* w;                // NULL: no weight
-  int H;
-  int ctas;                     // CTAs that take this side's tiles
-  int tile;                     // tokens of a tile
-  // the CTA's lane groups take `toks` tokens at a time, `gp` groups to a token, each `per` of its
-  // heads one after another (so that a lane keeps the token's angles in registers)
-  int gp, per, toks;
-  long long next_head, next_tok;   // elements from a row to the group's next one
+  int H;                        // 0: no such side
+  uint32_t inv_h;               // ceil(2^32 / H) for H > 1: row / H is the high half of row * inv_h, exactly for
+                                // row * H < 2^32 (inv_h * H exceeds 2^32 by less than H)
   float* part;                  // backward with a weight: [ctas][D] partial sums
 };
 
@@ -56,6 +54,8 @@ struct Params {
   const int* pos;
   const float* inv_freq;
   int tokens, N, D, R, pos0, interleaved, norm;
+  int tile;                     // tokens whose cos and sin are held at a time
+  int ctas_q;                   // backward: CTAs of q, the others take k
   float eps, af;
 };
 
@@ -115,6 +115,9 @@ __device__ __forceinline__ void store8<__half>(__half* p, const float2 (&f)[4]) 
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ void store1(float* p, float f) { *p = f; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void store1(__half* p, float f) { *p = __float2half_rn(f); }
@@ -134,15 +137,27 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 struct Angles {
   float2 c[4], s[4];
 };
-__device__ __forceinline__ void get_angles(Angles& g, const float* cosr, const float* sinr, int c0, int c1,
+// Where a token's table holds frequency f: interleaved, in order; else the first four of each
+// eight before the last four, so that neighbouring lanes read neighbouring 16 bytes.
+__device__ __forceinline__ int tab_pos(int f, int R, int interleaved) {
+  return interleaved ? f : ((f & 4) / 4 * (R / 16) + f / 8) * 4 + f % 4;
+}
+__device__ __forceinline__ void get_angles(Angles& g, const float* cosr, const float* sinr, int c0, int c1, int R,
                                            int interleaved) {
-  const int f0 = interleaved ? 4 * c0 : 8 * c0, f1 = interleaved ? 4 * c1 : 8 * c0 + 4;
+  const int f0 = 4 * c0, f1 = interleaved ? 4 * c1 : 4 * (R / 16 + c0);
   const float4 a = *reinterpret_cast<const float4*>(cosr + f0), b = *reinterpret_cast<const float4*>(cosr + f1);
   const float4 u = *reinterpret_cast<const float4*>(sinr + f0), v = *reinterpret_cast<const float4*>(sinr + f1);
   g.c[0] = make_float2(a.x, a.y), g.c[1] = make_float2(a.z, a.w);
   g.c[2] = make_float2(b.x, b.y), g.c[3] = make_float2(b.z, b.w);
   g.s[0] = make_float2(u.x, u.y), g.s[1] = make_float2(u.z, u.w);
   g.s[2] = make_float2(v.x, v.y), g.s[3] = make_float2(v.z, v.w);
+}
+
+// Weights of chunk c.
+__device__ __forceinline__ void get_weights(float2 (&w)[4], const float* ws, int c, int D) {
+  const float4 u = *reinterpret_cast<const float4*>(ws + 4 * c), v = *reinterpret_cast<const float4*>(ws + D / 2 + 4 * c);
+  w[0] = make_float2(u.x, u.y), w[1] = make_float2(u.z, u.w);
+  w[2] = make_float2(v.x, v.y), w[3] = make_float2(v.z, v.w);
 }
 
 // Turns the pairs of chunks c0 (a) and c1 (b); BACK by the negated angles.
@@ -172,83 +187,83 @@ __device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const Angle
   }
 }
 
-// LPR lanes hold a row (a power of two >= D/16; lanes beyond D/16 idle).
+// LPR lanes hold a row (a power of two >= D/16; lanes beyond D/16 idle).  Forward: a CTA takes the
+// q and k rows of its tokens, which share the angles.  Backward: of one side, whose dw it sums.
 template <typename T, int LPR, bool BWD>
-__global__ void __launch_bounds__(THREADS, BWD ? 2 : 3) norm_rope_kernel(const __grid_constant__ Params p) {
-  extern __shared__ __align__(16) float tab[];     // cos [tile][R/2], then sin
+__global__ void __launch_bounds__(THREADS, BWD ? BWD_CTAS : FWD_CTAS) norm_rope_kernel(const __grid_constant__ Params p) {
   constexpr int ROWS = THREADS / LPR;              // rows of one step of the CTA
-  const int side = (int)blockIdx.x < p.s[0].ctas ? 0 : 1;
-  const Side& s = p.s[side];
-  const int cta = (int)blockIdx.x - (side ? p.s[0].ctas : 0);
+  extern __shared__ __align__(16) float smem[];    // weights [2][D], cos [tile][R/2], sin; backward, at the end: sums
   const int lane = threadIdx.x % LPR, row0 = threadIdx.x / LPR;
-  const int D = p.D, R = p.R, H = s.H, half = R / 2;
+  const int D = p.D, R = p.R, half = R / 2;
   const bool has = lane < D / 16;
   const bool rot = lane < R / 16;
   const int c0 = rot ? lane : R / 8 + 2 * (lane - R / 16);
   const int c1 = rot ? lane + R / 16 : c0 + 1;
-  float2 w0[4], w1[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) w0[e] = w1[e] = both(1.0f);
-  if (s.w && has) {
-    Raw<T> r;
-    load_raw(r, static_cast<const T*>(s.w) + 8 * c0);
-    unpack(r, w0);
-    load_raw(r, static_cast<const T*>(s.w) + 8 * c1);
-    unpack(r, w1);
+  const float inv_d = 1.0f / (float)D;
+  // (the sum of dw may be scheduled now; it waits for this whole grid)
+  if (BWD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int side = BWD && (int)blockIdx.x >= p.ctas_q ? 1 : 0;
+  const int cta = (int)blockIdx.x - (side ? p.ctas_q : 0);
+  const int ctas = BWD ? (side ? (int)gridDim.x - p.ctas_q : p.ctas_q) : (int)gridDim.x;
+  // weights in fp32, the first four of each eight before the last four
+  float* ws = smem;
+  float* cos_tab = smem + 2 * D;
+  float* sin_tab = cos_tab + p.tile * half;
+  for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
+    const int sd = i / D, d = i - sd * D;
+    ws[sd * D + ((d & 4) / 4 * (D / 8) + d / 8) * 4 + d % 4] =
+        p.s[sd].w ? to_float(static_cast<const T*>(p.s[sd].w)[d]) : 1.0f;
   }
   float2 dw0[4], dw1[4];
   if (BWD) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw0[e] = dw1[e] = both(0.0f);
   }
-  const float inv_d = 1.0f / (float)D;
-  // this CTA's tokens, equal shares; a tile of them has its cos and sin in shared memory
-  const int tok_begin = (int)((long long)p.tokens * cta / s.ctas);
-  const int tok_end = (int)((long long)p.tokens * (cta + 1) / s.ctas);
-  const bool need_x = !BWD || p.norm;
-  for (int tok0 = tok_begin; tok0 < tok_end; tok0 += s.tile) {
-    const int n_tok = min(s.tile, tok_end - tok0);
-    const size_t base = (size_t)tok0 * H * D;
-    const T* x = static_cast<const T*>(s.x) + base;
-    const T* dy = static_cast<const T*>(s.dy) + base;
-    T* y = static_cast<T*>(s.y) + base;
-    // a row's loads go out one step before it is worked on, the first ones before the angles
+  // this CTA's tokens, an equal share
+  const int tok_begin = (int)((long long)p.tokens * cta / ctas);
+  const int tok_end = (int)((long long)p.tokens * (cta + 1) / ctas);
+  for (int tok0 = tok_begin; tok0 < tok_end; tok0 += p.tile) {
+    const int n_tok = min(p.tile, tok_end - tok0);
+    // rows [0, n0) are of the first side, [n0, n_rows) of k
+    const int n0 = n_tok * p.s[side].H, n_rows = BWD ? n0 : n0 + n_tok * p.s[1].H;
+    auto elem = [&](int r) {     // its first element in its side's tensors
+      const int sd = BWD ? side : r < n0 ? 0 : 1;
+      return ((size_t)tok0 * p.s[sd].H + (!BWD && sd ? r - n0 : r)) * D;
+    };
     Raw<T> xa, xb, ya, yb;
-    auto fetch = [&](int tok, size_t off) {
-      if (!has || tok >= n_tok) return;
-      if (need_x) {
-        load_raw(xa, x + off + 8 * c0);
-        load_raw(xb, x + off + 8 * c1);
+    auto fetch = [&](int r) {
+      if (!has || r >= n_rows) return;
+      const size_t off = elem(r);
+      const Side& s = p.s[BWD ? side : r < n0 ? 0 : 1];
+      if (!BWD || p.norm) {
+        load_raw(xa, static_cast<const T*>(s.x) + off + 8 * c0);
+        load_raw(xb, static_cast<const T*>(s.x) + off + 8 * c1);
       }
       if (BWD) {
-        load_raw(ya, dy + off + 8 * c0);
-        load_raw(yb, dy + off + 8 * c1);
+        load_raw(ya, static_cast<const T*>(s.dy) + off + 8 * c0);
+        load_raw(yb, static_cast<const T*>(s.dy) + off + 8 * c1);
       }
     };
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) xa.v[i] = xb.v[i] = ya.v[i] = yb.v[i] = make_uint4(0, 0, 0, 0);
-    int tok = row0 / s.gp, k = 0;
-    size_t off = ((size_t)tok * H + row0 % s.gp) * D;
-    fetch(tok, off);
+    fetch(row0);                 // on their way while the angles are computed
     __syncthreads();
-    float* sin_tab = tab + n_tok * half;
     for (int i = threadIdx.x; i < n_tok * half; i += THREADS) {
       const int tk = i / half, f = i - tk * half;
       const int pos = p.pos ? p.pos[tok0 + tk] : p.pos0 + (tok0 + tk) % p.N;
       const double turns = (double)pos * (double)p.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
       float sn, cn;
       sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
-      tab[i] = cn * p.af;
-      sin_tab[i] = sn * p.af;
+      const int at = tk * half + tab_pos(f, R, p.interleaved);
+      cos_tab[at] = cn * p.af;
+      sin_tab[at] = sn * p.af;
     }
     __syncthreads();
-    Angles g;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) g.c[e] = both(1.0f), g.s[e] = both(0.0f);
-    const int steps = (n_tok + s.toks - 1) / s.toks * s.per;   // the same for every lane
-    for (int i = 0; i < steps; ++i) {
-      const bool live = has && tok < n_tok;
-      const size_t at = off;
+    for (int r0 = 0; r0 < n_rows; r0 += ROWS) {   // the same trip count for every lane
+      const int r = r0 + row0;
+      const bool live = has && r < n_rows;
+      const int sd = BWD ? side : r < n0 ? 0 : 1;
+      const Side& s = p.s[sd];
       float2 a[4], b[4], ga[4], gb[4];
       unpack(xa, a);
       unpack(xb, b);
@@ -256,71 +271,71 @@ __global__ void __launch_bounds__(THREADS, BWD ? 2 : 3) norm_rope_kernel(const _
         unpack(ya, ga);
         unpack(yb, gb);
       }
-      if (k == 0 && rot && live) get_angles(g, tab + tok * half, sin_tab + tok * half, c0, c1, p.interleaved);
-      if (++k == s.per) {
-        k = 0;
-        tok += s.toks;
-        off += s.next_tok;
-      } else {
-        off += s.next_head;
-      }
-      fetch(tok, off);
+      fetch(r + ROWS);
       float rstd = 1.0f;
+      const float* w = ws + sd * D;
+      float2 w0[4], w1[4];
       if (p.norm) {
         float2 ss = both(0.0f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss = __ffma2_rn(a[e], a[e], __ffma2_rn(b[e], b[e], ss));
         rstd = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_d + p.eps);
+        if (has) {
+          get_weights(w0, w, c0, D);
+          get_weights(w1, w, c1, D);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {   // xhat
           a[e] = __fmul2_rn(a[e], both(rstd));
           b[e] = __fmul2_rn(b[e], both(rstd));
         }
       }
-      if (!BWD) {
-        if (p.norm) {
+      if (!BWD && p.norm) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] = __fmul2_rn(a[e], w0[e]);
-            b[e] = __fmul2_rn(b[e], w1[e]);
-          }
+        for (int e = 0; e < 4; ++e) {
+          a[e] = __fmul2_rn(a[e], w0[e]);
+          b[e] = __fmul2_rn(b[e], w1[e]);
         }
-        if (rot) turn<false>(a, b, g, p.interleaved);
-        if (live) {
-          store8(y + at + 8 * c0, a);
-          store8(y + at + 8 * c1, b);
-        }
-      } else {
-        if (rot) turn<true>(ga, gb, g, p.interleaved);
-        if (p.norm) {
-          float2 dot2 = both(0.0f);
+      }
+      if (rot && live) {
+        const int in_side = !BWD && sd ? r - n0 : r;
+        const int tk = s.H == 1 ? in_side : (int)__umulhi((uint32_t)in_side, s.inv_h);
+        Angles g;
+        get_angles(g, cos_tab + tk * half, sin_tab + tk * half, c0, c1, R, p.interleaved);
+        if (BWD)
+          turn<true>(ga, gb, g, p.interleaved);
+        else
+          turn<false>(a, b, g, p.interleaved);
+      }
+      if (BWD && p.norm) {
+        float2 dot2 = both(0.0f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (live) {     // behind its last row a lane holds that row's values still
-              dw0[e] = __ffma2_rn(ga[e], a[e], dw0[e]);
-              dw1[e] = __ffma2_rn(gb[e], b[e], dw1[e]);
-            }
+        for (int e = 0; e < 4; ++e) {
+          if (live) {     // behind its last row a lane holds that row's values still
+            dw0[e] = __ffma2_rn(ga[e], a[e], dw0[e]);
+            dw1[e] = __ffma2_rn(gb[e], b[e], dw1[e]);
             ga[e] = __fmul2_rn(ga[e], w0[e]);
             gb[e] = __fmul2_rn(gb[e], w1[e]);
-            dot2 = __ffma2_rn(ga[e], a[e], __ffma2_rn(gb[e], b[e], dot2));
           }
-          const float dot = row_sum<LPR>(dot2.x + dot2.y) * inv_d;
+          dot2 = __ffma2_rn(ga[e], a[e], __ffma2_rn(gb[e], b[e], dot2));
+        }
+        const float dot = row_sum<LPR>(dot2.x + dot2.y) * inv_d;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ga[e] = __fmul2_rn(both(rstd), __ffma2_rn(a[e], both(-dot), ga[e]));
-            gb[e] = __fmul2_rn(both(rstd), __ffma2_rn(b[e], both(-dot), gb[e]));
-          }
+        for (int e = 0; e < 4; ++e) {
+          ga[e] = __fmul2_rn(both(rstd), __ffma2_rn(a[e], both(-dot), ga[e]));
+          gb[e] = __fmul2_rn(both(rstd), __ffma2_rn(b[e], both(-dot), gb[e]));
         }
-        if (live) {
-          store8(y + at + 8 * c0, ga);
-          store8(y + at + 8 * c1, gb);
-        }
+      }
+      if (live) {
+        T* y = static_cast<T*>(s.y) + elem(r);
+        store8(y + 8 * c0, BWD ? ga : a);
+        store8(y + 8 * c1, BWD ? gb : b);
       }
     }
   }
-  if (BWD && s.part) {   // the CTA's sums, rows in order
-    float* red = tab;                              // [ROWS][D]
+  if (BWD && p.s[side].part) {   // the CTA's sums, lane groups in order
     __syncthreads();
+    float* red = smem;           // [ROWS][D]
     if (has) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -332,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, BWD ? 2 : 3) norm_rope_kernel(const _
     for (int d = threadIdx.x; d < D; d += THREADS) {
       float sum = 0.0f;
       for (int r = 0; r < ROWS; ++r) sum += red[r * D + d];
-      s.part[(size_t)cta * D + d] = sum;
+      p.s[side].part[(size_t)cta * D + d] = sum;
     }
   }
 }
@@ -349,6 +364,7 @@ __global__ void __launch_bounds__(256) dw_sum_kernel(const __grid_constant__ Sum
   __shared__ float red[32][8];
   const int side = blockIdx.y, col = (int)blockIdx.x * 8 + threadIdx.x % 8, slice = threadIdx.x / 8;
   float sum = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (a.part[side])
     for (int i = slice; i < a.n[side]; i += 32) sum += a.part[side][(size_t)i * a.D + col];
   red[slice][threadIdx.x % 8] = sum;
@@ -360,65 +376,43 @@ __global__ void __launch_bounds__(256) dw_sum_kernel(const __grid_constant__ Sum
   }
 }
 
-size_t smem_bytes(const Params& p, int lpr, bool bwd) {
-  size_t tab = 0;
-  for (int i = 0; i < 2; ++i)
-    if (p.s[i].ctas) tab = std::max(tab, (size_t)p.s[i].tile * (p.R / 2) * 2 * sizeof(float));
-  const size_t red = bwd ? (size_t)(THREADS / lpr) * p.D * sizeof(float) : 0;
-  return std::max(tab, red);
-}
-
 template <typename T, int LPR>
-cudaError_t launch_lpr(const Params& p, bool bwd, cudaStream_t st) {
-  const int grid = p.s[0].ctas + p.s[1].ctas;
-  const size_t smem = smem_bytes(p, LPR, bwd);   // at most 32 KB
+cudaError_t launch_lpr(const Params& p, int grid, bool bwd, cudaStream_t st) {
+  const size_t tab = (2 * p.D + (size_t)p.tile * p.R) * sizeof(float);      // at most 18 KB
   if (bwd)
-    norm_rope_kernel<T, LPR, true><<<grid, THREADS, smem, st>>>(p);
+    norm_rope_kernel<T, LPR, true>
+        <<<grid, THREADS, std::max(tab, (size_t)(THREADS / LPR) * p.D * sizeof(float)), st>>>(p);
   else
-    norm_rope_kernel<T, LPR, false><<<grid, THREADS, smem, st>>>(p);
+    norm_rope_kernel<T, LPR, false><<<grid, THREADS, tab, st>>>(p);
   return cudaGetLastError();
 }
 
 int lanes(int D) { return D <= 64 ? 4 : D <= 128 ? 8 : 16; }
 
 template <typename T>
-cudaError_t launch_type(const Params& p, bool bwd, cudaStream_t st) {
+cudaError_t launch_type(const Params& p, int grid, bool bwd, cudaStream_t st) {
   switch (lanes(p.D)) {
-    case 4: return launch_lpr<T, 4>(p, bwd, st);
-    case 8: return launch_lpr<T, 8>(p, bwd, st);
-    default: return launch_lpr<T, 16>(p, bwd, st);
+    case 4: return launch_lpr<T, 4>(p, grid, bwd, st);
+    case 8: return launch_lpr<T, 8>(p, grid, bwd, st);
+    default: return launch_lpr<T, 16>(p, grid, bwd, st);
   }
 }
 
-// CTAs of each side and the tokens of a tile.  A CTA should have at least a few steps of rows to
-// share its cos and sin among, unless there are too few tokens to give every SM one.
-void plan(Params& p, int n_sm, int max_ctas) {
-  const int rows = THREADS / lanes(p.D);
-  const int heads = p.s[0].H + p.s[1].H;
-  for (int i = 0; i < 2; ++i) {
-    Side& s = p.s[i];
-    if (!s.H) {
-      s.ctas = 0;
-      continue;
-    }
-    const long long tile = std::max(1LL, 4LL * rows / s.H);          // tokens of four steps
-    const long long share = std::max(1LL, (long long)max_ctas * s.H / heads);
-    const long long one_each = std::max(1LL, 4LL * n_sm * s.H / heads);
-    const long long least = std::max(1LL, (long long)rows / s.H);    // tokens of one step
-    long long ctas = std::max(((long long)p.tokens + tile - 1) / tile,
-                              std::min(((long long)p.tokens + least - 1) / least, one_each));
-    s.ctas = (int)std::min(ctas, share);
-    const long long toks = ((long long)p.tokens + s.ctas - 1) / s.ctas;
-    s.tile = (int)(p.R ? std::min(toks, (long long)MAX_TAB / (p.R / 2)) : toks);
-    // at least two heads a group where there are two: neighbouring groups then read neighbouring
-    // rows, and a step of the CTA spans few tokens
-    s.gp = 1;
-    while (s.H % (2 * s.gp) == 0 && s.H / (2 * s.gp) >= 2 && 2 * s.gp <= rows) s.gp *= 2;
-    s.per = s.H / s.gp;
-    s.toks = rows / s.gp;
-    s.next_head = (long long)s.gp * p.D;
-    s.next_tok = (long long)s.toks * s.H * p.D - (s.per - 1) * s.next_head;
-  }
+// CTAs for `heads` heads a token, at most `most`: with few tokens one step of rows each, so that
+// every SM has work; else at least four steps, which share the angles.
+int ctas_for(const Params& p, int heads, long long least, long long most) {
+  const long long rows = THREADS / lanes(p.D), all = (long long)p.tokens * heads;
+  const long long fine = std::min((all + rows - 1) / rows, least), coarse = (all + 4 * rows - 1) / (4 * rows);
+  return (int)std::max(1LL, std::min({(long long)p.tokens, std::max(fine, coarse), most}));
+}
+
+// Tokens of a tile: a CTA's share, as far as the angles and the division by H (see Side) go.
+int tile_for(const Params& p, int ctas) {
+  long long t = ((long long)p.tokens + ctas - 1) / ctas;
+  if (p.R) t = std::min(t, (long long)MAX_TAB / (p.R / 2));
+  for (const Side& s : p.s)
+    if (s.H > 1) t = std::min(t, ((1ll << 32) - 1) / ((long long)s.H * s.H));
+  return (int)t;
 }
 
 Params make(const NormRopeArgs& a) {
@@ -431,42 +425,55 @@ Params make(const NormRopeArgs& a) {
   p.pos = a.positions, p.inv_freq = a.inv_freq;
   p.tokens = a.B * a.N, p.N = a.N, p.D = a.D, p.R = a.R, p.pos0 = a.pos0;
   p.interleaved = a.interleaved, p.norm = a.norm, p.eps = a.eps, p.af = a.attn_factor;
+  for (Side& s : p.s)
+    if (s.H > 1) s.inv_h = (uint32_t)(((1ull << 32) + s.H - 1) / s.H);
   return p;
 }
 
-cudaError_t launch(const Params& p, int dtype, bool bwd, cudaStream_t st) {
-  if (dtype == S2ATTN_BF16) return launch_type<__nv_bfloat16>(p, bwd, st);
-  if (dtype == S2ATTN_FP16) return launch_type<__half>(p, bwd, st);
-  return launch_type<float>(p, bwd, st);
+cudaError_t launch(const Params& p, int grid, int dtype, bool bwd, cudaStream_t st) {
+  if (dtype == S2ATTN_BF16) return launch_type<__nv_bfloat16>(p, grid, bwd, st);
+  if (dtype == S2ATTN_FP16) return launch_type<__half>(p, grid, bwd, st);
+  return launch_type<float>(p, grid, bwd, st);
 }
 
 }  // namespace nr
 
 cudaError_t launch_norm_rope_fwd(const NormRopeArgs& a, int n_sm, cudaStream_t st) {
   nr::Params p = nr::make(a);
-  nr::plan(p, n_sm, nr::FWD_CTAS * n_sm);
-  return nr::launch(p, a.dtype, false, st);
+  const int grid = nr::ctas_for(p, p.s[0].H + p.s[1].H, 2 * n_sm, (long long)nr::FWD_CTAS * n_sm);
+  p.tile = nr::tile_for(p, grid);
+  return nr::launch(p, grid, a.dtype, false, st);
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* part, int n_sm, cudaStream_t st) {
   nr::Params p = nr::make(a);
-  nr::plan(p, n_sm, std::min(kNormRopePartials, nr::BWD_CTAS * n_sm));
+  const long long heads = p.s[0].H + p.s[1].H, most = std::min(kNormRopePartials, nr::BWD_CTAS * n_sm);
+  int ctas[2];
+  for (int i = 0; i < 2; ++i)
+    ctas[i] = p.s[i].H ? nr::ctas_for(p, p.s[i].H, 2 * n_sm * p.s[i].H / heads, std::max(1LL, most * p.s[i].H / heads)) : 0;
+  p.ctas_q = ctas[0];
+  p.tile = nr::tile_for(p, ctas[0] && ctas[1] ? std::min(ctas[0], ctas[1]) : ctas[0] + ctas[1]);
   if (a.dwq && p.s[0].H) p.s[0].part = part;
-  if (a.dwk && p.s[1].H) p.s[1].part = part + (size_t)p.s[0].ctas * a.D;
-  cudaError_t e = nr::launch(p, a.dtype, true, st);
+  if (a.dwk && p.s[1].H) p.s[1].part = part + (size_t)ctas[0] * a.D;
+  cudaError_t e = nr::launch(p, ctas[0] + ctas[1], a.dtype, true, st);
   if (e != cudaSuccess || (!p.s[0].part && !p.s[1].part)) return e;
   nr::SumArgs s{};
   s.D = a.D;
   void* dw[2] = {a.dwq, a.dwk};
-  for (int i = 0; i < 2; ++i) s.part[i] = p.s[i].part, s.dw[i] = dw[i], s.n[i] = p.s[i].ctas;
-  const dim3 grid(a.D / 8, 2);
-  if (a.dtype == S2ATTN_BF16)
-    nr::dw_sum_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(s);
-  else if (a.dtype == S2ATTN_FP16)
-    nr::dw_sum_kernel<__half><<<grid, 256, 0, st>>>(s);
-  else
-    nr::dw_sum_kernel<float><<<grid, 256, 0, st>>>(s);
-  return cudaGetLastError();
+  for (int i = 0; i < 2; ++i) s.part[i] = p.s[i].part, s.dw[i] = dw[i], s.n[i] = ctas[i];
+  // a programmatic dependent launch: scheduled while the backward drains
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.D / 8, 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (a.dtype == S2ATTN_BF16) return cudaLaunchKernelEx(&cfg, nr::dw_sum_kernel<__nv_bfloat16>, s);
+  if (a.dtype == S2ATTN_FP16) return cudaLaunchKernelEx(&cfg, nr::dw_sum_kernel<__half>, s);
+  return cudaLaunchKernelEx(&cfg, nr::dw_sum_kernel<float>, s);
 }
 
 }  // namespace s2
