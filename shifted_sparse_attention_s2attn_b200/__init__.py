@@ -408,7 +408,7 @@ def lora_proj_bwd(x, w, lora_a, lora_b, dy, dx, d_lora_a, d_lora_b, parts, scali
 
 def _fit(t, name, shape, dtype, dev):
     """A contiguous tensor of this shape and dtype on device `dev` (an index, -1 for the host)."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         where = f"cuda:{dev}" if dev >= 0 else "the host"
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {where} "
                          "like the other tensors")
@@ -437,9 +437,14 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
-def _dtype_code(t, name, f32):
-    torch = _torch()
-    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype, 3)
+_dtype_codes = {}
+
+
+def _dtype_code(dtype, name, f32):
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _dtype_codes.get(dtype, 3)
     if code > (2 if f32 else 1):
         raise ValueError(f"{name} must be bf16{', fp16 or fp32' if f32 else ' or fp16'}")
     return code
@@ -469,44 +474,35 @@ def rope_inv_freq(R, base=10000.0, scaling="none", factor=1.0, original_len=4096
     return out, af.value
 
 
-def _norm_rope_args(sides, inv_freq, wq, wk, norm, positions, pos0):
-    """Checks a call's sides [(name, tensor, [(name, tensor like it)])] for q and k: the sizes, the
-    type's code and the device."""
-    torch = _torch()
-    ref = sides[0][1] if sides[0][1] is not None else sides[1][1]
+def _norm_rope_ref(q, k, names, norm, wq, wk, inv_freq, positions, pos0):
+    """Checks what a call's sides share, q and k being the tensors that give their sizes; q's (or
+    without it k's) shape, type and device."""
+    ref = k if q is None else q
     if ref is None:
-        raise ValueError("q or k must be given")
-    if ref.dim() != 4:
-        raise ValueError("q and k must be [B,N,H,D]")
-    B, N, _, D = ref.shape
-    dt, dev = ref.dtype, ref.get_device()
-    heads = []
-    for name, t, likes in sides:
-        if t is None:
-            if any(o is not None for _, o in likes):
-                raise ValueError(f"{name} must be given with its output or gradient")
-            heads.append(0)
-            continue
-        H = t.shape[2] if t.dim() == 4 else 1
-        shape = (B, N, H, D)
-        _fit(t, name, shape, dt, dev)
-        for like, o in likes:
-            if o is None:
-                raise ValueError(f"{like} must be given with {name}")
-            _fit(o, like, shape, dt, dev)
-        heads.append(H)
-    if wq is not None or wk is not None:
-        if not norm:
-            raise ValueError("wq and wk are only used with norm=True")
-        for name, w in (("wq", wq), ("wk", wk)):
-            if w is not None:
-                _fit(w, name, (D,), dt, dev)
-    _fit(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, dev)
+        raise ValueError(f"{names[0]} or {names[1]} must be given")
+    shape, dtype, dev = ref.shape, ref.dtype, ref.get_device()
+    if len(shape) != 4:
+        raise ValueError(f"{names[0]} and {names[1]} must be [B,N,H,D]")
+    if wq is not None:
+        _fit(wq, "wq", shape[3:], dtype, dev)
+    if wk is not None:
+        _fit(wk, "wk", shape[3:], dtype, dev)
+    if not norm and (wq is not None or wk is not None):
+        raise ValueError("wq and wk are only used with norm=True")
+    f32 = _torch().float32
+    if inv_freq.dim() != 1 or inv_freq.dtype is not f32 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous fp32 vector on the device of the other tensors")
     if positions is not None:
-        _fit(positions, "positions", (B, N), torch.int32, dev)
-    if not -2 ** 31 <= pos0 < 2 ** 31 - N:
+        _fit(positions, "positions", shape[:2], _torch().int32, dev)
+    elif not -2 ** 31 <= pos0 < 2 ** 31 - shape[1]:
         raise ValueError("pos0 is outside the range of positions")
-    return B, N, heads[0], heads[1], D, 2 * inv_freq.numel(), _dtype_code(ref, "q/k", True), dev
+    return shape, dtype, dev
+
+
+def _norm_rope_k_shape(shape, k, name):
+    if k.dim() != 4:
+        raise ValueError(f"{name} must be [B,N,H,D]")
+    return shape[0], shape[1], k.shape[2], shape[3]
 
 
 def qk_norm_rope_fwd(q, k, q_out, k_out, inv_freq, wq=None, wk=None, norm=True, eps=1e-6, positions=None, pos0=0,
@@ -515,11 +511,23 @@ def qk_norm_rope_fwd(q, k, q_out, k_out, inv_freq, wq=None, wk=None, norm=True, 
     embedding of its first 2*len(inv_freq) elements, in one pass, into q_out and k_out (which
     may be q and k).  q with q_out, or k with k_out, may be None.  wq, wk [D] (None: 1);
     positions [B,N] int32 (None: pos0 + row); bf16, fp16 or fp32."""
-    B, N, Hq, Hk, D, R, dt, dev = _norm_rope_args((("q", q, (("q_out", q_out),)), ("k", k, (("k_out", k_out),))),
-                                                  inv_freq, wq, wk, norm, positions, pos0)
+    shape, dtype, dev = _norm_rope_ref(q, k, ("q", "k"), norm, wq, wk, inv_freq, positions, pos0)
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out, and k and k_out, must be given together")
+    Hq = Hk = 0
+    if q is not None:
+        Hq = shape[2]
+        _fit(q, "q", shape, dtype, dev)
+        _fit(q_out, "q_out", shape, dtype, dev)
+    if k is not None:
+        k_shape = _norm_rope_k_shape(shape, k, "k")
+        Hk = k_shape[2]
+        _fit(k, "k", k_shape, dtype, dev)
+        _fit(k_out, "k_out", k_shape, dtype, dev)
     _call_on(dev, "qk_norm_rope_fwd", stream, _adr(q), _adr(k), _adr(wq), _adr(wk), _adr(positions),
-             inv_freq.data_ptr(), _adr(q_out), _adr(k_out), B, N, Hq, Hk, D, R, bool(interleaved), bool(norm), eps,
-             attn_factor, pos0, dt)
+             inv_freq.data_ptr(), _adr(q_out), _adr(k_out), shape[0], shape[1], Hq, Hk, shape[3], 2 * inv_freq.numel(),
+             bool(interleaved), bool(norm), eps, attn_factor, 0 if positions is not None else pos0,
+             _dtype_code(dtype, "q/k", True))
 
 
 def qk_norm_rope_bwd_workspace_bytes(D):
@@ -531,23 +539,40 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, inv_freq, wq=None, wk=None, d
     """Backward of qk_norm_rope_fwd: dq, dk (which may be dq_out, dk_out) and, where given, dwq, dwk
     [D].  q, k are the forward's inputs (norm=False: may be None).  workspace: a uint8 device
     tensor of qk_norm_rope_bwd_workspace_bytes(D) bytes, needed with dwq or dwk."""
-    if norm:
-        sides = (("dq_out", dq_out, (("dq", dq), ("q", q))), ("dk_out", dk_out, (("dk", dk), ("k", k))))
-    else:
+    shape, dtype, dev = _norm_rope_ref(dq_out, dk_out, ("dq_out", "dk_out"), norm, wq, wk, inv_freq, positions, pos0)
+    if (dq_out is None) != (dq is None) or (dk_out is None) != (dk is None):
+        raise ValueError("dq_out and dq, and dk_out and dk, must be given together")
+    if not norm:
         q = k = None
-        sides = (("dq_out", dq_out, (("dq", dq),)), ("dk_out", dk_out, (("dk", dk),)))
-    B, N, Hq, Hk, D, R, dt, dev = _norm_rope_args(sides, inv_freq, wq, wk, norm, positions, pos0)
+    elif (q is None) != (dq is None) or (k is None) != (dk is None):
+        raise ValueError("with norm=True q must be given with dq, and k with dk")
+    Hq = Hk = 0
+    if dq_out is not None:
+        Hq = shape[2]
+        _fit(dq_out, "dq_out", shape, dtype, dev)
+        _fit(dq, "dq", shape, dtype, dev)
+        if norm:
+            _fit(q, "q", shape, dtype, dev)
+    if dk_out is not None:
+        k_shape = _norm_rope_k_shape(shape, dk_out, "dk_out")
+        Hk = k_shape[2]
+        _fit(dk_out, "dk_out", k_shape, dtype, dev)
+        _fit(dk, "dk", k_shape, dtype, dev)
+        if norm:
+            _fit(k, "k", k_shape, dtype, dev)
     ws, ws_bytes = None, 0
     if dwq is not None or dwk is not None:
-        for name, d, g in (("dwq", dwq, dq), ("dwk", dwk, dk)):
-            if d is not None:
-                if not norm or g is None:
-                    raise ValueError(f"{name} needs norm=True and its side's gradient")
-                _fit(d, name, (D,), g.dtype, dev)
+        if not norm or (dwq is not None and dq is None) or (dwk is not None and dk is None):
+            raise ValueError("dwq and dwk need norm=True and their side's gradient")
+        if dwq is not None:
+            _fit(dwq, "dwq", shape[3:], dtype, dev)
+        if dwk is not None:
+            _fit(dwk, "dwk", shape[3:], dtype, dev)
         ws, ws_bytes = _scratch(workspace, dev)
     _call_on(dev, "qk_norm_rope_bwd", stream, _adr(q), _adr(k), _adr(dq_out), _adr(dk_out), _adr(wq), _adr(wk),
-             _adr(positions), inv_freq.data_ptr(), _adr(dq), _adr(dk), _adr(dwq), _adr(dwk), B, N, Hq, Hk, D, R,
-             bool(interleaved), bool(norm), eps, attn_factor, pos0, dt, ws, ws_bytes)
+             _adr(positions), inv_freq.data_ptr(), _adr(dq), _adr(dk), _adr(dwq), _adr(dwk), shape[0], shape[1], Hq, Hk,
+             shape[3], 2 * inv_freq.numel(), bool(interleaved), bool(norm), eps, attn_factor,
+             0 if positions is not None else pos0, _dtype_code(dtype, "q/k", True), ws, ws_bytes)
 
 
 def s2attn_tree_mask(parents, mask, depth=None, stream=None):
@@ -598,7 +623,7 @@ def s2attn_tree_decode(q, k_new, v_new, k_pages, v_pages, page_table, cache_len,
     B, M, H, D = q.shape
     Hkv = k_new.shape[2]
     dtype, dev = q.dtype, q.get_device()
-    code = _dtype_code(q, "q", False)
+    code = _dtype_code(dtype, "q", False)
     _fit(q, "q", (B, M, H, D), dtype, dev)
     _fit(o, "o", (B, M, H, D), dtype, dev)
     _fit(k_new, "k_new", (B, M, Hkv, D), dtype, dev)
@@ -624,7 +649,7 @@ def s2attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, r
         raise ValueError("k_new must be [B,M,Hkv,D]")
     B, M, Hkv, D = k_new.shape
     dtype, dev = k_new.dtype, k_new.get_device()
-    _dtype_code(k_new, "k_new", True)
+    _dtype_code(dtype, "k_new", True)
     _fit(k_new, "k_new", (B, M, Hkv, D), dtype, dev)
     _fit(v_new, "v_new", (B, M, Hkv, D), dtype, dev)
     n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype, dev)
@@ -652,7 +677,7 @@ def s2attn_cache_copy_pages(pools, pairs, stream=None):
     if len(shape) < 2:
         raise ValueError("a pool must be [n_pages, ...]")
     for t in pools:
-        if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
             _fit(t, "every pool", shape, dtype, dev)
     addresses = array.array("Q", [t.data_ptr() for t in pools])
     flat = array.array("i", bytes(8 * len(pairs)))
