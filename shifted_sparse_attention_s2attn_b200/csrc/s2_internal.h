@@ -145,7 +145,6 @@ struct TreePlan {
   int RT;         // row tiles
   int J;          // runs a unit's key tiles are cut into
   int slot_rows;  // rows of a partial
-  int BN;         // keys of a tile: 64 or 128
 };
 struct TreeMaps {
   CUtensorMap q, k_pages, v_pages, k_new, v_new;

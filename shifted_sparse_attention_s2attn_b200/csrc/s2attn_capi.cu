@@ -779,7 +779,7 @@ int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, cons
   a.cache_len = cache_len, a.new_len = new_len, a.page_table = page_table, a.mask = tree_mask, a.v_new = v_new;
   a.B = B, a.M = M, a.H = H, a.Hkv = Hkv, a.D = D, a.page_shift = page_shift_of(page_size);
   a.n_pages = n_pages, a.width = table_width, a.dtype = dtype, a.err = err, a.index_err = err + 1;
-  const int page_box = std::min(page_size, t.BN), new_box = std::min(M, t.BN);
+  const int page_box = page_size < 64 ? page_size : 64, new_box = M < 64 ? M : 64;
   s2::TreeMaps maps;
   if (!map_heads(&maps.q, q, dtype, (long long)B * M, H, D, t.group, t.tok < M ? t.tok : M) ||
       !map_heads(&maps.k_pages, k_pages, dtype, (long long)n_pages * page_size, Hkv, D, 1, page_box) ||

@@ -42,36 +42,27 @@
 #include "s2_ptx.cuh"
 #include "s2attn.h"
 
-#ifndef BN_RULE
-#define BN_RULE 64
-#endif
 namespace s2 {
 namespace tree {
 
-constexpr int BM = 128;
+constexpr int BM = 128, BN = 64;
+constexpr int KST = 2, VST = 2;              // ring stages
 constexpr int NTHREADS = 224;
 constexpr int WARP_K = 4, WARP_V = 5, WARP_MMA = 6;
 constexpr uint32_t QBOX = BM * 128;          // 128 rows x 128 B (64 columns)
-constexpr int MAXST = 2;                     // ring stages, at most
-constexpr int NBARS = 2 + 4 * MAXST + 2 + 2 + 5;
+constexpr uint32_t KBOX = BN * 128;
+constexpr int NBARS = 2 + 2 * KST + 2 * VST + 2 + 2 + 5;
 constexpr int kSeqCost = 3;                  // of a sequence's end, in key tiles
 constexpr uint32_t TM_COLS = 256;
 constexpr uint32_t TM_O = 128;               // S buffers at columns 0 and 64
 
-// HD: head dimension; BN: keys of a tile.  With 64 keys S has two buffers (S(i) is computed while
-// the softmax works on S(i-1)) and K and V two stages each; with 128 one of each, and the other
-// CTA of the SM fills the time.
-template <int HD_, int BN_>
+template <int HD>
 struct Cfg {
-  static constexpr int HD = HD_, BN = BN_;
   static constexpr int NB = HD / 64;         // 64-column boxes of a row
-  static constexpr int NS = 128 / BN;        // S buffers
-  static constexpr int NST = HD * BN <= 64 * 128 ? 2 : 1;   // ring stages of K and of V
-  static constexpr uint32_t KBOX = BN * 128; // BN rows x 128 B
   static constexpr uint32_t QTILE = NB * QBOX, KTILE = NB * KBOX;
   static constexpr uint32_t OFF_K = QTILE;
-  static constexpr uint32_t OFF_V = OFF_K + NST * KTILE;
-  static constexpr uint32_t OFF_BAR = OFF_V + NST * KTILE;
+  static constexpr uint32_t OFF_V = OFF_K + KST * KTILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + VST * KTILE;
   static constexpr uint32_t OFF_MISC = OFF_BAR + NBARS * 8;   // tmem address, abort flag, run
   static constexpr uint32_t OFF_LEN = OFF_MISC + 128;         // int len[kTreeMaxB], then new[kTreeMaxB]
   static constexpr uint32_t SMEM = OFF_LEN + 2 * kTreeMaxB * 4;
@@ -104,22 +95,18 @@ __device__ __forceinline__ int cap_tokens(const Params& p) {
 }
 
 // Key tiles of the cache, and of the drafted tokens, that sequence b contributes.
-template <int BN>
 __device__ __forceinline__ int cache_tiles(int len) { return (int)(((long long)len + BN - 1) / BN); }
-template <int BN>
 __device__ __forceinline__ int all_tiles(int len, int nw, int first_tok) {
-  return nw > first_tok ? cache_tiles<BN>(len) + (nw + BN - 1) / BN : 0;
+  return nw > first_tok ? cache_tiles(len) + (nw + BN - 1) / BN : 0;
 }
 
 // Keys of tile t of a sequence.
-template <int BN>
 __device__ __forceinline__ int tile_keys(int t, int len, int nw) {
-  const int ct = cache_tiles<BN>(len);
+  const int ct = cache_tiles(len);
   return t < ct ? min(BN, len - t * BN) : min(BN, nw - (t - ct) * BN);
 }
 
 // Walks the segments of a run: `b` and its tiles [t0, t0 + n) of `total`.
-template <int BN>
 struct Segments {
   const int* len;
   const int* nw;
@@ -132,7 +119,7 @@ struct Segments {
       t0 = 0;
     }
     if (left <= 0) return false;
-    while ((total = all_tiles<BN>(len[b], nw[b], first_tok)) == 0) ++b;
+    while ((total = all_tiles(len[b], nw[b], first_tok)) == 0) ++b;
     n = min(left, total - t0);
     left -= n;
     return true;
@@ -169,8 +156,8 @@ __device__ __forceinline__ bool elect_one() {
   return x != 0;
 }
 
-// S[128 x BN] = Q K^T, both K-major.
-template <int HD, uint32_t KBOX>
+// S[128 x 64] = Q K^T, both K-major.
+template <int HD>
 __device__ __forceinline__ void issue_s(uint32_t d, uint32_t sq, uint32_t sk, uint32_t idesc) {
   const uint64_t dq = sdesc_sw128(sq, 16, 1024), dk = sdesc_sw128(sk, 16, 1024);
 #pragma unroll
@@ -179,8 +166,8 @@ __device__ __forceinline__ void issue_s(uint32_t d, uint32_t sq, uint32_t sk, ui
            kk > 0 ? 1u : 0u);
 }
 
-// O[128 x HD] (+)= P V over the tile's first 16 * KSTEPS keys: P from TMEM, V seen MN-major.
-template <int KSTEPS, uint32_t KBOX>
+// O[128 x HD] (+)= P V over 16 * KSTEPS keys: P from TMEM, V seen MN-major.
+template <int KSTEPS>
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t tp, uint32_t sv, uint32_t idesc, bool first) {
   const uint64_t dv = sdesc_sw128(sv, KBOX, 1024);
 #pragma unroll
@@ -211,27 +198,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Max of a row's 64 scores and `mx` over the columns whose bit of (lo, hi) is set (MASK).
-template <bool MASK>
-__device__ __forceinline__ float row_max(const uint32_t (&s)[64], uint32_t lo, uint32_t hi, float mx) {
-  float m[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m[e] = mx;
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    float x = __uint_as_float(s[2 * c]), y = __uint_as_float(s[2 * c + 1]);
-    if (MASK) {
-      const uint32_t w = c < 16 ? lo : hi;
-      x = (w >> (2 * c % 32)) & 1u ? x : -INFINITY;
-      y = (w >> (2 * c % 32 + 1)) & 1u ? y : -INFINITY;
-    }
-    m[c % 8] = max3(m[c % 8], x, y);
-  }
-  return fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])));
-}
-
-// 64 columns of a P row = exp2(s * sl2 - m), zero in columns whose bit of (lo, hi) is clear (MASK),
-// as 16-bit pairs into 32 columns of the row's S buffer; returns their fp32 sum.
+// P row = exp2(s * sl2 - m), zero in columns whose bit of (lo, hi) is clear (MASK), as 16-bit
+// pairs over the first 32 columns of the row's S buffer; returns the fp32 row sum.
 template <bool FP16, bool MASK>
 __device__ __forceinline__ float p_row(const uint32_t (&sr)[64], uint32_t lo, uint32_t hi, float sl2, float neg_m,
                                        uint32_t t_s) {
@@ -244,24 +212,24 @@ __device__ __forceinline__ float p_row(const uint32_t (&sr)[64], uint32_t lo, ui
   for (int c = 0; c < 32; ++c) {
     const float2 x =
         __ffma2_rn(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), scale2, shift2);
-    float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+    float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
     if (MASK) {
       const uint32_t w = c < 16 ? lo : hi;
-      p0 = (w >> (2 * c % 32)) & 1u ? p0 : 0.f;
-      p1 = (w >> (2 * c % 32 + 1)) & 1u ? p1 : 0.f;
+      e.x = (w >> (2 * c % 32)) & 1u ? e.x : 0.f;
+      e.y = (w >> (2 * c % 32 + 1)) & 1u ? e.y : 0.f;
     }
-    sp[c % 4].x += p0;
-    sp[c % 4].y += p1;
-    pk[c] = pack16<FP16>(p0, p1);
+    sp[c % 4] = __fadd2_rn(sp[c % 4], e);
+    pk[c] = pack16<FP16>(e.x, e.y);
   }
   tmem_st_x32(t_s, pk);
-  return ((sp[0].x + sp[1].x) + (sp[2].x + sp[3].x)) + ((sp[0].y + sp[1].y) + (sp[2].y + sp[3].y));
+  const float2 a = __fadd2_rn(__fadd2_rn(sp[0], sp[1]), __fadd2_rn(sp[2], sp[3]));
+  return a.x + a.y;
 }
 
 // Clears V rows behind the `keep` of a tile that the product reads (it goes in steps of 16) and,
-// with `scan`, the elements of the others that are infinite or NaN, whose rows it notes in bad[].  Row r of column box x lies at
+// with `scan`, the elements of the others that are infinite or NaN, whose rows it notes in bad[2].  Row r of column box x lies at
 // x * KBOX + r * 128 whatever the swizzle, which only permutes 16-byte pieces of the row.
-template <int HD, uint32_t KBOX, bool FP16>
+template <int HD, bool FP16>
 __device__ __forceinline__ void clean_v(uint8_t* v, int keep, bool scan, uint32_t* bad, int tid, int nthreads) {
   const uint32_t exp_mask = FP16 ? 0x7c00u : 0x7f80u;
   const int rows = (keep + 15) & ~15;
@@ -287,23 +255,21 @@ __device__ __forceinline__ void clean_v(uint8_t* v, int keep, bool scan, uint32_
   }
 }
 
-template <int HD, int BN, bool FP16>
+template <int HD, bool FP16>
 __global__ void __launch_bounds__(NTHREADS, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkp,
                 const __grid_constant__ CUtensorMap tvp, const __grid_constant__ CUtensorMap tkn,
                 const __grid_constant__ CUtensorMap tvn, const Params p) {
-  using C = Cfg<HD, BN>;
-  constexpr int NST = C::NST, NS = C::NS;
-  constexpr uint32_t KBOX = C::KBOX;
+  using C = Cfg<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;
-  uint64_t* k_empty = k_full + NST;
-  uint64_t* v_full = k_empty + NST;
-  uint64_t* v_empty = v_full + NST;
-  uint64_t* s_full = v_empty + NST;     // [2]
+  uint64_t* k_empty = k_full + KST;
+  uint64_t* v_full = k_empty + KST;
+  uint64_t* v_empty = v_full + VST;
+  uint64_t* s_full = v_empty + VST;     // [2]
   uint64_t* p_ready = s_full + 2;       // [2]
   uint64_t* pv_done = s_full + 4;
   uint64_t* o_full = s_full + 5;
@@ -341,9 +307,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int s = 0; s < NST; ++s) {
+    for (int s = 0; s < KST; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
@@ -382,7 +350,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     // tiles, the output, the next Q).  The run takes the tiles of an equal share of the weights.
     int sum = 0, weight = 0;       // the host has checked that these fit
     for (int b = lane; b < p.B; b += 32) {
-      const int n = all_tiles<BN>(s_len[b], s_new[b], first_tok);
+      const int n = all_tiles(s_len[b], s_new[b], first_tok);
       sum += n;
       weight += n ? n + kSeqCost : 0;
     }
@@ -395,7 +363,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     int b0 = 0, t0 = 0, at0 = -1, at1 = -1, tiles_before = 0, weight_before = 0;
     for (int base = 0; base < p.B && j < runs; base += 32) {
       const int b = base + lane;
-      const int n = b < p.B ? all_tiles<BN>(s_len[b], s_new[b], first_tok) : 0;
+      const int n = b < p.B ? all_tiles(s_len[b], s_new[b], first_tok) : 0;
       int ti = n, wi = n ? n + kSeqCost : 0;      // inclusive sums over the lanes
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -434,7 +402,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   const int n_tiles = run[2];
   const bool skip = *abort_flag != 0 || n_tiles == 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Segments<BN> seg(s_len, s_new, first_tok, run[0], run[1], n_tiles);
+  Segments seg(s_len, s_new, first_tok, run[0], run[1], n_tiles);
 
   if (!skip && (warp == WARP_K || warp == WARP_V)) {
     // ---------------- producers: Q and K, or V ----------------
@@ -444,12 +412,14 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     uint64_t* full = is_k ? k_full : v_full;
     uint64_t* empty = is_k ? k_empty : v_empty;
     uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+    constexpr int NST = KST;
+    static_assert(KST == VST, "one ring depth");
     const int box_keys = min(1 << p.page_shift, BN);
     const int new_box = min(p.M, BN);
     bool ok = true;
     int i = 0, n_seg = 0;
     while (ok && seg.next()) {
-      const int b = seg.b, len = s_len[b], ct = cache_tiles<BN>(len);
+      const int b = seg.b, len = s_len[b], ct = cache_tiles(len);
       const int used = (int)(((long long)len + (1 << p.page_shift) - 1) >> p.page_shift);
       if (is_k) {
         // Q rows (token, head of the group) of the row tile
@@ -514,7 +484,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     }
     __syncwarp();
   } else if (!skip && warp == WARP_MMA) {
-    // ---------------- MMA issuer ----------------
+    // ---------------- MMA issuer: S(i) | P(i-1) V(i-1) ----------------
     // The whole warp walks the tiles and one elected lane issues: where the compiler sees that
     // one lane runs, an MMA's operands go straight to uniform registers (P V of a tile: 423 ->
     // 130 cycles to issue, against `if (lane == 0)`).
@@ -525,9 +495,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     bool ok = true;
     int ns = 0, np = 0;             // segments whose S, whose first PV was issued
     int s_left = 0, pv_left = 0;    // tiles left in the segment of S and of PV
-    Segments<BN> sp(s_len, s_new, first_tok, run[0], run[1], n_tiles);
-    // step i: S(i), then P V of tile i - (NS - 1)
-    for (int i = 0; i < n_tiles + NS - 1 && ok; ++i) {
+    Segments sp(s_len, s_new, first_tok, run[0], run[1], n_tiles);
+    for (int i = 0; i <= n_tiles && ok; ++i) {
       if (i < n_tiles) {
         if (s_left == 0) {
           seg.next();
@@ -535,20 +504,20 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           ok = wait_spin_warp(q_full, ns & 1, abort_flag, p.err);
           ++ns;
         }
-        if (ok) ok = wait_spin_warp(&k_full[i % NST], (i / NST) & 1, abort_flag, p.err);
+        if (ok) ok = wait_spin_warp(&k_full[i % KST], (i / KST) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
         --s_left;
         if (elect_one()) {
-          issue_s<HD, KBOX>(tmem + (uint32_t)BN * (i % NS), sq, sk + (i % NST) * C::KTILE, id_s);
-          mma_commit(&s_full[i % NS]);
-          mma_commit(&k_empty[i % NST]);
+          issue_s<HD>(tmem + (uint32_t)BN * (i & 1), sq, sk + (i % KST) * C::KTILE, id_s);
+          mma_commit(&s_full[i & 1]);
+          mma_commit(&k_empty[i % KST]);
           if (s_left == 0) mma_commit(q_empty);
         }
         __syncwarp();
       }
-      const int t = i - (NS - 1);
-      if (t >= 0) {
+      if (i > 0) {
+        const int t = i - 1;
         bool first = false;
         if (pv_left == 0) {
           sp.next();
@@ -557,24 +526,23 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           if (np > 0) ok = wait_spin_warp(o_free, (np - 1) & 1, abort_flag, p.err);   // O of the last segment read
           ++np;
         }
-        if (ok) ok = wait_spin_warp(&p_ready[t % NS], (t / NS) & 1, abort_flag, p.err);
-        if (ok) ok = wait_spin_warp(&v_full[t % NST], (t / NST) & 1, abort_flag, p.err);
+        if (ok) ok = wait_spin_warp(&p_ready[t & 1], (t >> 1) & 1, abort_flag, p.err);
+        if (ok) ok = wait_spin_warp(&v_full[t % VST], (t / VST) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
-        // whole tiles are issued as one run of MMAs (a test between them costs 100 cycles each)
-        const int ksteps = (tile_keys<BN>(sp.t0 + sp.n - pv_left, s_len[sp.b], s_new[sp.b]) + 15) / 16;
-        const uint32_t d_o = tmem + TM_O, tp = tmem + (uint32_t)BN * (t % NS), v0 = sv + (t % NST) * C::KTILE;
+        // a whole tile is one run of MMAs; the last tile's product stops behind its last key
+        const int ksteps = (tile_keys(sp.t0 + sp.n - pv_left, s_len[sp.b], s_new[sp.b]) + 15) / 16;
+        const uint32_t d_o = tmem + TM_O, tp = tmem + (uint32_t)BN * (t & 1), v0 = sv + (t % VST) * C::KTILE;
         --pv_left;
         if (elect_one()) {
           if (ksteps == BN / 16) {
-            issue_pv<BN / 16, KBOX>(d_o, tp, v0, id_pv, first);
+            issue_pv<BN / 16>(d_o, tp, v0, id_pv, first);
           } else {
 #pragma unroll 1
-            for (int kk = 0; kk < ksteps; ++kk)
-              issue_pv<1, KBOX>(d_o, tp + kk * 8, v0 + kk * 2048, id_pv, first && kk == 0);
+            for (int kk = 0; kk < ksteps; ++kk) issue_pv<1>(d_o, tp + kk * 8, v0 + kk * 2048, id_pv, first && kk == 0);
           }
           mma_commit(pv_done);
-          mma_commit(&v_empty[t % NST]);
+          mma_commit(&v_empty[t % VST]);
           if (pv_left == 0) mma_commit(o_full);
         }
         __syncwarp();
@@ -599,7 +567,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     bool ok = true;
     int i = 0, n_seg = 0, n_draft = 0;
     while (ok && seg.next()) {
-      const int b = seg.b, len = s_len[b], nw = s_new[b], ct = cache_tiles<BN>(len);
+      const int b = seg.b, len = s_len[b], nw = s_new[b], ct = cache_tiles(len);
       const bool row_ok = in_tile && m < nw;
       uint32_t* bad_rows = bad + 4 * (n_draft % 3);        // of this sequence's drafted tiles
       const bool has_draft = seg.t0 + seg.n > ct;
@@ -617,42 +585,49 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       }
       float m_run = -INFINITY, l_run = 0.f;
       for (int t = seg.t0; t < seg.t0 + seg.n && ok; ++t, ++i) {
-        const int buf = i % NS;
-        // keys of the tile, and which of them the row sees (a word per 64 columns)
+        const int buf = i & 1;
+        // keys of the tile, and which of them the row sees
         const bool draft = t >= ct;
-        const int keep = tile_keys<BN>(t, len, nw);
+        const int keep = tile_keys(t, len, nw);
         const bool edge = draft || keep < BN;
-        unsigned long long vis[BN / 64];
-#pragma unroll
-        for (int w = 0; w < BN / 64; ++w) vis[w] = ~0ull;
-        ok = wait_warp(&s_full[buf], (i / NS) & 1, abort_flag, p.err);
+        uint32_t lo = 0xffffffffu, hi = 0xffffffffu;
+        ok = wait_warp(&s_full[buf], (i >> 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
         if (edge) {
-#pragma unroll
-          for (int w = 0; w < BN / 64; ++w) {
-            const int n = keep - 64 * w;
-            vis[w] = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
-            if (draft) vis[w] &= BN == 128 ? see[w] : t == ct ? see[0] : see[1];
-          }
+          unsigned long long vis = keep >= 64 ? ~0ull : (1ull << keep) - 1ull;
+          if (draft) vis &= t == ct ? see[0] : see[1];
+          lo = (uint32_t)vis;
+          hi = (uint32_t)(vis >> 32);
           // V(i): only now, behind the wait for S(i).  That was issued after the product that read
           // the slot's last tile, so the slot's barrier is at most one phase back; before, it might
           // be two, and a wait by parity would take the older phase for this one.
-          ok = wait_warp(&v_full[i % NST], (i / NST) & 1, abort_flag, p.err);
+          ok = wait_warp(&v_full[i % VST], (i / VST) & 1, abort_flag, p.err);
           if (!ok) break;
-          clean_v<HD, KBOX, FP16>(smem + C::OFF_V + (i % NST) * C::KTILE, keep, draft,
-                                  bad_rows + (draft ? (t - ct) * (BN / 32) : 0), threadIdx.x, n_act * 32);
+          clean_v<HD, FP16>(smem + C::OFF_V + (i % VST) * C::KTILE, keep, draft, bad_rows + 2 * (draft ? t - ct : 0),
+                            threadIdx.x, n_act * 32);
           fence_proxy_async_smem();
         }
         const uint32_t t_s = lane_addr + (uint32_t)BN * buf;
         uint32_t s0[64];
-        float mx = -INFINITY;
+        tmem_ld_x64(t_s, s0);
+        float mxp[8];
 #pragma unroll
-        for (int w = BN / 64 - 1; w >= 0; --w) {      // the first 64 columns stay in registers
-          tmem_ld_x64(t_s + 64 * w, s0);
-          mx = edge ? row_max<true>(s0, (uint32_t)vis[w], (uint32_t)(vis[w] >> 32), mx)
-                    : row_max<false>(s0, 0, 0, mx);
+        for (int e = 0; e < 8; ++e) mxp[e] = -INFINITY;
+        if (!edge) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            mxp[c % 8] = max3(mxp[c % 8], __uint_as_float(s0[2 * c]), __uint_as_float(s0[2 * c + 1]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint32_t w = c < 16 ? lo : hi;
+            mxp[c % 8] = max3(mxp[c % 8], (w >> (2 * c % 32)) & 1u ? __uint_as_float(s0[2 * c]) : -INFINITY,
+                              (w >> (2 * c % 32 + 1)) & 1u ? __uint_as_float(s0[2 * c + 1]) : -INFINITY);
+          }
         }
+        const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
+                               fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
         // the running max moves only when it grows by more than 2^8 (P then stays below 2^8,
         // inside fp16's range too); a row that has seen no key keeps -inf and its P stays 0
         const float m_new = fmaxf(m_run, mx * sl2);
@@ -661,12 +636,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
         if (need) m_run = m_new;
         l_run *= alpha;
-#pragma unroll
-        for (int w = 0; w < BN / 64; ++w) {           // P over columns of S that have been read
-          if (w > 0) tmem_ld_x64(t_s + 64 * w, s0);
-          l_run += edge ? p_row<FP16, true>(s0, (uint32_t)vis[w], (uint32_t)(vis[w] >> 32), sl2, -m_run, t_s + 32 * w)
-                        : p_row<FP16, false>(s0, 0, 0, sl2, -m_run, t_s + 32 * w);
-        }
+        l_run += edge ? p_row<FP16, true>(s0, lo, hi, sl2, -m_run, t_s) : p_row<FP16, false>(s0, lo, hi, sl2, -m_run, t_s);
         if (rescale && t > seg.t0) {
           // O was last written by the previous tile's product: wait for it, then scale the row
           ok = wait_warp(pv_done, (i - 1) & 1, abort_flag, p.err);
@@ -735,7 +705,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       if (st_ok && (fix[0] | fix[1] | fix[2] | fix[3])) {
         // add the infinities and NaN that clean_v took out, to what this thread has just written
 #pragma unroll 1
-        for (int key = 0; key < kTreeMaxM; ++key) {
+        for (int key = 0; key < 2 * BN; ++key) {
           const uint32_t w = key < 64 ? (key < 32 ? fix[0] : fix[1]) : (key < 96 ? fix[2] : fix[3]);
           if (!((w >> (key % 32)) & 1u)) continue;
           const uint16_t* v = static_cast<const uint16_t*>(p.v_new) + (((size_t)b * p.M + key) * p.Hkv + kvh) * HD;
@@ -871,9 +841,9 @@ __global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_cons
         a.mx == -INFINITY ? -INFINITY : (a.mx + log2f(a.L)) * 0.69314718055994531f;
 }
 
-template <int HD, int BN, bool FP16>
+template <int HD, bool FP16>
 cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
-  using C = Cfg<HD, BN>;
+  using C = Cfg<HD>;
   // the shared-memory limit is a per-device function attribute: set it once per device
   static std::atomic<uint64_t> done_mask{0};
   int dev = 0;
@@ -881,12 +851,12 @@ cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
   if (!bit || !(done_mask.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(tree_kernel<HD, BN, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    e = cudaFuncSetAttribute(tree_kernel<HD, FP16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     done_mask.fetch_or(bit, std::memory_order_acq_rel);
   }
   const unsigned grid = (unsigned)(p.Hkv * p.RT * p.J);
-  tree_kernel<HD, BN, FP16><<<grid, NTHREADS, C::SMEM, st>>>(t.q, t.k_pages, t.v_pages, t.k_new, t.v_new, p);
+  tree_kernel<HD, FP16><<<grid, NTHREADS, C::SMEM, st>>>(t.q, t.k_pages, t.v_pages, t.k_new, t.v_new, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.J == 1) return e;   // one run: every sequence was written whole
   cudaLaunchConfig_t cfg = {};
@@ -906,11 +876,6 @@ cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, tree_combine_kernel<HD, FP16>, p, ws, rp);
 }
 
-template <int HD, bool FP16>
-cudaError_t launch_tile(const TreeMaps& t, const Params& p, int BN, cudaStream_t st) {
-  return BN == 128 ? launch<HD, 128, FP16>(t, p, st) : launch<HD, 64, FP16>(t, p, st);
-}
-
 }  // namespace tree
 
 // Row tiles and runs.  A unit's J CTAs should fill whole waves of two CTAs an SM: the J up to
@@ -922,7 +887,6 @@ TreePlan tree_plan(int M, int H, int Hkv) {
   t.tok = tree::BM / t.group;
   t.RT = (M + t.tok - 1) / t.tok;
   const long long U = (long long)Hkv * t.RT;
-  t.BN = BN_RULE;
   t.slot_rows = (t.tok < M ? t.tok : M) * t.group;
   t.J = 1;
   double best = 1e30;
@@ -946,8 +910,8 @@ cudaError_t launch_tree_decode(const TreeMaps& maps, const TreeArgs& a, const Tr
   p.sl2 = (float)(1.4426950408889634 / std::sqrt((double)a.D));
   p.err = a.err, p.index_err = a.index_err;
   const bool fp16 = a.dtype == S2ATTN_FP16;
-  if (a.D == 128) return fp16 ? tree::launch_tile<128, true>(maps, p, t.BN, st) : tree::launch_tile<128, false>(maps, p, t.BN, st);
-  return fp16 ? tree::launch_tile<64, true>(maps, p, t.BN, st) : tree::launch_tile<64, false>(maps, p, t.BN, st);
+  if (a.D == 128) return fp16 ? tree::launch<128, true>(maps, p, st) : tree::launch<128, false>(maps, p, st);
+  return fp16 ? tree::launch<64, true>(maps, p, st) : tree::launch<64, false>(maps, p, st);
 }
 
 }  // namespace s2
