@@ -202,3 +202,35 @@ def test_captured_on_a_stream_and_replayed():
     s2.qk_norm_rope_fwd(d["q"], d["k"], *want, d["inv_freq"], **how)
     no_device_error()
     assert torch.equal(q_out, want[0]) and torch.equal(k_out, want[1])
+
+
+def test_more_than_two_to_the_31_elements():
+    """The last rows of a tensor of more than 2^31 elements, forward and backward."""
+    N, H, D = 132000, 128, 128
+    assert N * H * D > 2 ** 31
+    q = torch.zeros(1, N, H, D, dtype=BF, device="cuda")
+    g = torch.Generator().manual_seed(0)
+    tail = torch.randn(1, 3, H, D, generator=g).to(BF)
+    q[:, -3:] = tail.cuda()
+    f = s2.rope_inv_freq(D)[0]
+    out = torch.empty_like(q)
+    s2.qk_norm_rope_fwd(q, None, out, None, f.cuda())
+    no_device_error()
+    pos = torch.arange(N - 3, N)[None]
+    want, scale = norm_rope(tail, None, pos, f, True, 1e-6, 1.0, False)
+    check_close(out[:, -3:], want, HALF_STEP[BF] * want.abs() + 64 * 2.0 ** -24 * scale, "q")
+    s2.qk_norm_rope_bwd(q, None, q, None, out, None, f.cuda())
+    no_device_error()
+    want, scale, _, _ = norm_rope_grad(tail, None, tail, pos, f, True, 1e-6, 1.0, False)
+    check_close(out[:, -3:], want, HALF_STEP[BF] * want.abs() + 128 * 2.0 ** -24 * scale, "dq")
+
+
+def test_heads_at_the_limit():
+    """16384 heads (the division of a row by H is exact there) beside one."""
+    x = _inputs(1, 9, 16384, 1, 16, 16, F32, True, True)
+    d = _dev(x)
+    q_out, k_out = torch.empty_like(d["q"]), torch.empty_like(d["k"])
+    s2.qk_norm_rope_fwd(d["q"], d["k"], q_out, k_out, d["inv_freq"], wq=d["wq"], wk=d["wk"], positions=d["positions"],
+                        eps=1e-5)
+    no_device_error()
+    _fwd_check(x, q_out, k_out, True, 1e-5, 1.0, False)

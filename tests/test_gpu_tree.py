@@ -261,3 +261,96 @@ def test_agrees_with_the_contiguous_decoding_step():
     # sum p|v| <= max over keys of |v| < 5 times the sum of p; measured outputs are far smaller
     assert (o.float() - o2.float()).abs().max() <= 2.0 ** -8 * 2 * (o.float().abs().max() + 1)
     assert (lse - lse2).abs().max() <= 1e-4
+
+
+def test_every_mask_bit_set():
+    """Bits of tokens that do not exist (j >= new_len, j >= M) show nothing."""
+    B, M = 3, 70
+    c, _, _, new = _case([20, 0, 129], M, 4, 2, 64, 16, BF, "chain", new=[70, 33, 1])
+    see = torch.ones(B, M, M, dtype=torch.bool)
+    words = torch.full((B, M, 2), -1, dtype=torch.int64)
+    _check(c, see, words, new)
+
+
+def test_pages_behind_the_first_four_gigabytes():
+    """A pool of more than 2^32 bytes and 2^31 elements: the sequence's pages are its last ones."""
+    page, Hkv, D, H, M, n = 64, 8, 128, 8, 2, 150
+    n_pages = (2 ** 31 + 2 ** 24) // (page * Hkv * D)
+    c, see, words, new = _case([n], M, H, Hkv, D, page, BF, "chain", seed=3)
+    used = -(-n // page)
+    pools = []
+    for name in ("k_pages", "v_pages"):
+        pool = torch.zeros(n_pages, page, Hkv, D, dtype=BF, device="cuda")
+        ids = c["page_table"][0, :used].long()
+        pool[n_pages - used:] = c[name][ids].cuda()
+        pools.append(pool)
+    table = torch.arange(n_pages - used, n_pages, dtype=torch.int32, device="cuda")[None]
+    q, kn, vn, ln = (c[x].cuda() for x in ("q", "k_new", "v_new", "cache_len"))
+    o, lse = torch.empty_like(q), torch.empty(1, H, M, device="cuda")
+    ws = torch.empty(s2.s2attn_tree_decode_workspace_bytes(1, M, H, Hkv, D), dtype=torch.uint8, device="cuda")
+    s2.s2attn_tree_decode(q, kn, vn, *pools, table, ln, o, lse, ws)
+    no_device_error()
+    wo, wl, bo, bl = attend(*[c[x] for x in ("q", "k_new", "v_new", "k_pages", "v_pages", "page_table", "cache_len")],
+                            see, new)
+    check_close(o, wo, bo, "o")
+    check_close(lse, wl, bl, "lse")
+    # appended rows and copied pages beyond the same border
+    s2.s2attn_cache_append(kn, vn, *pools, table, ln)
+    s2.s2attn_cache_copy_pages(pools, [(n_pages - 1, 0), (1, n_pages - 2)])
+    no_device_error()
+    for pool, new_rows in zip(pools, (kn, vn)):
+        assert torch.equal(pool[n_pages - 1, n % page:n % page + M], new_rows[0])
+        assert torch.equal(pool[0].nan_to_num(), pool[n_pages - 1].nan_to_num()) and (pool[n_pages - 2] == 0).all()
+
+
+_FIRST_CALL = """
+import torch
+import shifted_sparse_attention_s2attn_b200 as s2
+B, M, H, Hk, D = 1, 2, 4, 2, 64
+q, kn = (torch.randn(B, M, h, D, device="cuda").half() for h in (H, Hk))
+pages = torch.randn(4, 16, Hk, D, device="cuda").half()
+table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+n = torch.tensor([40], dtype=torch.int32, device="cuda")
+o, lse = torch.zeros_like(q), torch.zeros(B, H, M, device="cuda")
+f = s2.rope_inv_freq(D)[0].cuda()
+ws = torch.empty(s2.s2attn_tree_decode_workspace_bytes(B, M, H, Hk, D), dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s2.qk_norm_rope_fwd(q, kn, q, kn, f, pos0=40)
+    s2.s2attn_tree_decode(q, kn, kn, pages, pages, table, n, o, lse, ws)
+    s2.s2attn_cache_append(kn, kn, pages, pages, table, n)
+g.replay()
+torch.cuda.synchronize()
+assert s2.get_device_error() == (0, 0)
+assert o.abs().sum() > 0 and torch.equal(pages[2, 8:10], kn[0])
+print("captured first call ok")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALL], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "captured first call ok" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_host_threads_at_once():
+    """Two threads, each with its own stream, workspace and inputs."""
+    import threading
+    cases = [_case([300, 40], 5, 8, 2, 128, 16, BF, "tree", seed=s) for s in (1, 2)]
+    want = [_run(c, w, n, False) for c, _, w, n in cases]
+    got = [None, None]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got[i] = _run(cases[i][0], cases[i][2], cases[i][3], False)
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    no_device_error()
+    for w, g in zip(want, got):
+        assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])

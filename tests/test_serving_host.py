@@ -29,7 +29,7 @@ def _fwd(lib, q=P, k=P, wq=NULL, wk=NULL, pos=NULL, f=P, qo=P, ko=P, B=1, N=8, H
 
 
 @pytest.mark.parametrize("bad", [
-    dict(B=0), dict(N=0), dict(Hq=0), dict(D=120), dict(D=272), dict(D=8, R=8), dict(R=144), dict(R=24), dict(R=-16),
+    dict(B=0), dict(N=0), dict(Hq=0), dict(Hk=16385), dict(D=120), dict(D=272), dict(D=8, R=8), dict(R=144), dict(R=24), dict(R=-16),
     dict(dtype=3), dict(dtype=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(af=float("inf")), dict(f=NULL),
     dict(q=NULL), dict(qo=NULL), dict(q=NULL, qo=NULL, k=NULL, ko=NULL), dict(q=P + 8), dict(ko=P + 4), dict(pos=P + 2),
     dict(wq=P, norm=0), dict(wk=P + 8), dict(B=1 << 16, N=1 << 15), dict(pos0=2 ** 31 - 4),
