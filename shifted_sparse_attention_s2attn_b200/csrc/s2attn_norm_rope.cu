@@ -115,9 +115,6 @@ __device__ __forceinline__ void store8<__half>(__half* p, const float2 (&f)[4]) 
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ void store1(float* p, float f) { *p = f; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float f) { *p = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void store1(__half* p, float f) { *p = __float2half_rn(f); }
@@ -153,13 +150,6 @@ __device__ __forceinline__ void get_angles(Angles& g, const float* cosr, const f
   g.s[2] = make_float2(v.x, v.y), g.s[3] = make_float2(v.z, v.w);
 }
 
-// Weights of chunk c.
-__device__ __forceinline__ void get_weights(float2 (&w)[4], const float* ws, int c, int D) {
-  const float4 u = *reinterpret_cast<const float4*>(ws + 4 * c), v = *reinterpret_cast<const float4*>(ws + D / 2 + 4 * c);
-  w[0] = make_float2(u.x, u.y), w[1] = make_float2(u.z, u.w);
-  w[2] = make_float2(v.x, v.y), w[3] = make_float2(v.z, v.w);
-}
-
 // Turns the pairs of chunks c0 (a) and c1 (b); BACK by the negated angles.
 __device__ __forceinline__ float2 turn_one(float2 x, float c, float s) {
   return make_float2(x.x * c - x.y * s, x.y * c + x.x * s);
@@ -192,61 +182,45 @@ __device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const Angle
 template <typename T, int LPR, bool BWD>
 __global__ void __launch_bounds__(THREADS, BWD ? BWD_CTAS : FWD_CTAS) norm_rope_kernel(const __grid_constant__ Params p) {
   constexpr int ROWS = THREADS / LPR;              // rows of one step of the CTA
-  extern __shared__ __align__(16) float smem[];    // weights [2][D], cos [tile][R/2], sin; backward, at the end: sums
+  extern __shared__ __align__(16) float smem[];    // cos [tile][R/2], sin; backward, at the end: sums
   const int lane = threadIdx.x % LPR, row0 = threadIdx.x / LPR;
   const int D = p.D, R = p.R, half = R / 2;
   const bool has = lane < D / 16;
   const bool rot = lane < R / 16;
   const int c0 = rot ? lane : R / 8 + 2 * (lane - R / 16);
   const int c1 = rot ? lane + R / 16 : c0 + 1;
+  const int apart = 8 * (c1 - c0);                 // elements from the lane's first chunk to its second
   const float inv_d = 1.0f / (float)D;
   // (the sum of dw may be scheduled now; it waits for this whole grid)
   if (BWD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int side = BWD && (int)blockIdx.x >= p.ctas_q ? 1 : 0;
   const int cta = (int)blockIdx.x - (side ? p.ctas_q : 0);
   const int ctas = BWD ? (side ? (int)gridDim.x - p.ctas_q : p.ctas_q) : (int)gridDim.x;
-  // weights in fp32, the first four of each eight before the last four
-  float* ws = smem;
-  float* cos_tab = smem + 2 * D;
+  float* cos_tab = smem;
   float* sin_tab = cos_tab + p.tile * half;
-  for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
-    const int sd = i / D, d = i - sd * D;
-    ws[sd * D + ((d & 4) / 4 * (D / 8) + d / 8) * 4 + d % 4] =
-        p.s[sd].w ? to_float(static_cast<const T*>(p.s[sd].w)[d]) : 1.0f;
-  }
   float2 dw0[4], dw1[4];
   if (BWD) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) dw0[e] = dw1[e] = both(0.0f);
   }
+  Raw<T> xa, xb, ya, yb;                           // a row's x and dy, one step ahead
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) xa.v[i] = xb.v[i] = ya.v[i] = yb.v[i] = make_uint4(0, 0, 0, 0);
+  auto fetch = [&](const T* x, const T* dy) {
+    if (!BWD || p.norm) {
+      load_raw(xa, x);
+      load_raw(xb, x + apart);
+    }
+    if (BWD) {
+      load_raw(ya, dy);
+      load_raw(yb, dy + apart);
+    }
+  };
   // this CTA's tokens, an equal share
   const int tok_begin = (int)((long long)p.tokens * cta / ctas);
   const int tok_end = (int)((long long)p.tokens * (cta + 1) / ctas);
   for (int tok0 = tok_begin; tok0 < tok_end; tok0 += p.tile) {
     const int n_tok = min(p.tile, tok_end - tok0);
-    // rows [0, n0) are of the first side, [n0, n_rows) of k
-    const int n0 = n_tok * p.s[side].H, n_rows = BWD ? n0 : n0 + n_tok * p.s[1].H;
-    auto elem = [&](int r) {     // its first element in its side's tensors
-      const int sd = BWD ? side : r < n0 ? 0 : 1;
-      return ((size_t)tok0 * p.s[sd].H + (!BWD && sd ? r - n0 : r)) * D;
-    };
-    Raw<T> xa, xb, ya, yb;
-    auto fetch = [&](int r) {
-      if (!has || r >= n_rows) return;
-      const size_t off = elem(r);
-      const Side& s = p.s[BWD ? side : r < n0 ? 0 : 1];
-      if (!BWD || p.norm) {
-        load_raw(xa, static_cast<const T*>(s.x) + off + 8 * c0);
-        load_raw(xb, static_cast<const T*>(s.x) + off + 8 * c1);
-      }
-      if (BWD) {
-        load_raw(ya, static_cast<const T*>(s.dy) + off + 8 * c0);
-        load_raw(yb, static_cast<const T*>(s.dy) + off + 8 * c1);
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) xa.v[i] = xb.v[i] = ya.v[i] = yb.v[i] = make_uint4(0, 0, 0, 0);
-    fetch(row0);                 // on their way while the angles are computed
     __syncthreads();
     for (int i = threadIdx.x; i < n_tok * half; i += THREADS) {
       const int tk = i / half, f = i - tk * half;
@@ -259,77 +233,91 @@ __global__ void __launch_bounds__(THREADS, BWD ? BWD_CTAS : FWD_CTAS) norm_rope_
       sin_tab[at] = sn * p.af;
     }
     __syncthreads();
-    for (int r0 = 0; r0 < n_rows; r0 += ROWS) {   // the same trip count for every lane
-      const int r = r0 + row0;
-      const bool live = has && r < n_rows;
-      const int sd = BWD ? side : r < n0 ? 0 : 1;
+#pragma unroll 1
+    for (int sd = side; sd < (BWD ? side + 1 : 2); ++sd) {
       const Side& s = p.s[sd];
-      float2 a[4], b[4], ga[4], gb[4];
-      unpack(xa, a);
-      unpack(xb, b);
-      if (BWD) {
-        unpack(ya, ga);
-        unpack(yb, gb);
-      }
-      fetch(r + ROWS);
-      float rstd = 1.0f;
-      const float* w = ws + sd * D;
+      const int n_rows = n_tok * s.H;
+      if (n_rows == 0) continue;
       float2 w0[4], w1[4];
-      if (p.norm) {
-        float2 ss = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ss = __ffma2_rn(a[e], a[e], __ffma2_rn(b[e], b[e], ss));
-        rstd = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_d + p.eps);
-        if (has) {
-          get_weights(w0, w, c0, D);
-          get_weights(w1, w, c1, D);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {   // xhat
-          a[e] = __fmul2_rn(a[e], both(rstd));
-          b[e] = __fmul2_rn(b[e], both(rstd));
-        }
+      for (int e = 0; e < 4; ++e) w0[e] = w1[e] = both(1.0f);
+      if (s.w && has) {
+        Raw<T> r;
+        load_raw(r, static_cast<const T*>(s.w) + 8 * c0);
+        unpack(r, w0);
+        load_raw(r, static_cast<const T*>(s.w) + 8 * c1);
+        unpack(r, w1);
       }
-      if (!BWD && p.norm) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] = __fmul2_rn(a[e], w0[e]);
-          b[e] = __fmul2_rn(b[e], w1[e]);
+      const size_t first = ((size_t)tok0 * s.H + row0) * D + 8 * c0;
+      const T* x = static_cast<const T*>(s.x) + first;
+      const T* dy = static_cast<const T*>(s.dy) + first;
+      T* y = static_cast<T*>(s.y) + first;
+      const int step = ROWS * D;
+      if (has && row0 < n_rows) fetch(x, dy);
+      for (int r = row0; r - row0 < n_rows; r += ROWS) {   // the same trip count for every lane
+        const bool live = has && r < n_rows;
+        float2 a[4], b[4], ga[4], gb[4];
+        unpack(xa, a);
+        unpack(xb, b);
+        if (BWD) {
+          unpack(ya, ga);
+          unpack(yb, gb);
         }
-      }
-      if (rot && live) {
-        const int in_side = !BWD && sd ? r - n0 : r;
-        const int tk = s.H == 1 ? in_side : (int)__umulhi((uint32_t)in_side, s.inv_h);
-        Angles g;
-        get_angles(g, cos_tab + tk * half, sin_tab + tk * half, c0, c1, R, p.interleaved);
-        if (BWD)
-          turn<true>(ga, gb, g, p.interleaved);
-        else
-          turn<false>(a, b, g, p.interleaved);
-      }
-      if (BWD && p.norm) {
-        float2 dot2 = both(0.0f);
+        x += step;
+        dy += step;
+        if (has && r + ROWS < n_rows) fetch(x, dy);
+        float rstd = 1.0f;
+        if (p.norm) {
+          float2 ss = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (live) {     // behind its last row a lane holds that row's values still
-            dw0[e] = __ffma2_rn(ga[e], a[e], dw0[e]);
-            dw1[e] = __ffma2_rn(gb[e], b[e], dw1[e]);
+          for (int e = 0; e < 4; ++e) ss = __ffma2_rn(a[e], a[e], __ffma2_rn(b[e], b[e], ss));
+          rstd = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_d + p.eps);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {   // xhat
+            a[e] = __fmul2_rn(a[e], both(rstd));
+            b[e] = __fmul2_rn(b[e], both(rstd));
+          }
+        }
+        if (!BWD && p.norm) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] = __fmul2_rn(a[e], w0[e]);
+            b[e] = __fmul2_rn(b[e], w1[e]);
+          }
+        }
+        if (rot && live) {
+          const int tk = s.H == 1 ? r : (int)__umulhi((uint32_t)r, s.inv_h);
+          Angles g;
+          get_angles(g, cos_tab + tk * half, sin_tab + tk * half, c0, c1, R, p.interleaved);
+          if (BWD)
+            turn<true>(ga, gb, g, p.interleaved);
+          else
+            turn<false>(a, b, g, p.interleaved);
+        }
+        if (BWD && p.norm) {
+          float2 dot2 = both(0.0f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (live) {     // behind its last row a lane holds that row's values still
+              dw0[e] = __ffma2_rn(ga[e], a[e], dw0[e]);
+              dw1[e] = __ffma2_rn(gb[e], b[e], dw1[e]);
+            }
             ga[e] = __fmul2_rn(ga[e], w0[e]);
             gb[e] = __fmul2_rn(gb[e], w1[e]);
+            dot2 = __ffma2_rn(ga[e], a[e], __ffma2_rn(gb[e], b[e], dot2));
           }
-          dot2 = __ffma2_rn(ga[e], a[e], __ffma2_rn(gb[e], b[e], dot2));
-        }
-        const float dot = row_sum<LPR>(dot2.x + dot2.y) * inv_d;
+          const float dot = row_sum<LPR>(dot2.x + dot2.y) * inv_d;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ga[e] = __fmul2_rn(both(rstd), __ffma2_rn(a[e], both(-dot), ga[e]));
-          gb[e] = __fmul2_rn(both(rstd), __ffma2_rn(b[e], both(-dot), gb[e]));
+          for (int e = 0; e < 4; ++e) {
+            ga[e] = __fmul2_rn(both(rstd), __ffma2_rn(a[e], both(-dot), ga[e]));
+            gb[e] = __fmul2_rn(both(rstd), __ffma2_rn(b[e], both(-dot), gb[e]));
+          }
         }
-      }
-      if (live) {
-        T* y = static_cast<T*>(s.y) + elem(r);
-        store8(y + 8 * c0, BWD ? ga : a);
-        store8(y + 8 * c1, BWD ? gb : b);
+        if (live) {
+          store8(y, BWD ? ga : a);
+          store8(y + apart, BWD ? gb : b);
+        }
+        y += step;
       }
     }
   }
@@ -378,7 +366,7 @@ __global__ void __launch_bounds__(256) dw_sum_kernel(const __grid_constant__ Sum
 
 template <typename T, int LPR>
 cudaError_t launch_lpr(const Params& p, int grid, bool bwd, cudaStream_t st) {
-  const size_t tab = (2 * p.D + (size_t)p.tile * p.R) * sizeof(float);      // at most 18 KB
+  const size_t tab = (size_t)p.tile * p.R * sizeof(float);      // at most 16 KB
   if (bwd)
     norm_rope_kernel<T, LPR, true>
         <<<grid, THREADS, std::max(tab, (size_t)(THREADS / LPR) * p.D * sizeof(float)), st>>>(p);
@@ -411,7 +399,7 @@ int tile_for(const Params& p, int ctas) {
   long long t = ((long long)p.tokens + ctas - 1) / ctas;
   if (p.R) t = std::min(t, (long long)MAX_TAB / (p.R / 2));
   for (const Side& s : p.s)
-    if (s.H > 1) t = std::min(t, ((1ll << 32) - 1) / ((long long)s.H * s.H));
+    if (s.H > 1) t = std::min({t, ((1ll << 32) - 1) / ((long long)s.H * s.H), (1ll << 30) / s.H});
   return (int)t;
 }
 

@@ -47,11 +47,11 @@ namespace tree {
 
 constexpr int BM = 128, BN = 64;
 constexpr int KST = 2, VST = 2;              // ring stages
-constexpr int NTHREADS = 224;
-constexpr int WARP_K = 4, WARP_V = 5, WARP_MMA = 6;
+constexpr int NTHREADS = 256;
+constexpr int WARP_K = 4, WARP_V = 5, WARP_S = 6, WARP_PV = 7;
 constexpr uint32_t QBOX = BM * 128;          // 128 rows x 128 B (64 columns)
 constexpr uint32_t KBOX = BN * 128;
-constexpr int NBARS = 2 + 2 * KST + 2 * VST + 2 + 2 + 5;
+constexpr int NBARS = 2 + 2 * KST + 2 * VST + 3 * 2 + 3 + 2;
 constexpr int kSeqCost = 3;                  // of a sequence's end, in key tiles
 constexpr uint32_t TM_COLS = 256;
 constexpr uint32_t TM_O = 128;               // S buffers at columns 0 and 64
@@ -271,11 +271,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   uint64_t* v_empty = v_full + VST;
   uint64_t* s_full = v_empty + VST;     // [2]
   uint64_t* p_ready = s_full + 2;       // [2]
-  uint64_t* pv_done = s_full + 4;
-  uint64_t* o_full = s_full + 5;
-  uint64_t* o_free = s_full + 6;
-  uint64_t* noted = s_full + 7;         // drafted rows with inf/NaN are noted
-  uint64_t* drain = s_full + 8;
+  uint64_t* pv_done = s_full + 4;       // [2]
+  uint64_t* o_full = s_full + 6;
+  uint64_t* o_free = s_full + 7;
+  uint64_t* noted = s_full + 8;         // drafted rows with inf/NaN are noted
+  uint64_t* drain = s_full + 9;         // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* run = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);        // sequence, tile, tiles, runs in use
@@ -318,12 +318,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_ready[s], n_act);
+      mbar_init(&pv_done[s], 1);
+      mbar_init(&drain[s], 1);
     }
-    mbar_init(pv_done, 1);
     mbar_init(o_full, 1);
     mbar_init(o_free, n_act);
     mbar_init(noted, n_act);
-    mbar_init(drain, 1);
     *abort_flag = (*(volatile int*)p.err != 0) ? 1 : 0;
     for (int i = 0; i < 12; ++i) bad[i] = 0;
     fence_mbar_init();
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     s_len[b] = lc;
     s_new[b] = nc;
   }
-  if (warp == WARP_MMA) {
+  if (warp == WARP_S) {
     tmem_alloc(tmem_slot, TM_COLS);
     tmem_relinquish();
   }
@@ -483,67 +483,66 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       if (!dok) report_error(p.err, (K_TREE << 8) | SITE_DRAIN);
     }
     __syncwarp();
-  } else if (!skip && warp == WARP_MMA) {
-    // ---------------- MMA issuer: S(i) | P(i-1) V(i-1) ----------------
-    // The whole warp walks the tiles and one elected lane issues: where the compiler sees that
-    // one lane runs, an MMA's operands go straight to uniform registers (P V of a tile: 423 ->
-    // 130 cycles to issue, against `if (lane == 0)`).
+  } else if (!skip && warp >= WARP_S) {
+    // ---------------- MMA issuers: S(i) = Q K(i), and P(i) V(i) ----------------
+    // A warp each: issuing blocks while the tensor pipe works off what is queued, and with one
+    // issuer S(i+1) waited behind P(i-1) V(i-1)'s issue as well as its execution.  Each warp
+    // walks the tiles as a whole and one elected lane issues: where the compiler sees that one
+    // lane runs, an MMA's operands go straight to uniform registers.
+    const bool is_s = warp == WARP_S;
     const uint32_t fmt = FP16 ? ~((1u << 7) | (1u << 10)) : ~0u;   // A and B formats: 0 = f16, 1 = bf16
     const uint32_t id_s = idesc_bf16_f32(BM, BN, false, false) & fmt;
     const uint32_t id_pv = idesc_bf16_f32(BM, HD, false, true) & fmt;
     const uint32_t sq = smem_u32(smem), sk = smem_u32(smem + C::OFF_K), sv = smem_u32(smem + C::OFF_V);
     bool ok = true;
-    int ns = 0, np = 0;             // segments whose S, whose first PV was issued
-    int s_left = 0, pv_left = 0;    // tiles left in the segment of S and of PV
-    Segments sp(s_len, s_new, first_tok, run[0], run[1], n_tiles);
-    for (int i = 0; i <= n_tiles && ok; ++i) {
-      if (i < n_tiles) {
-        if (s_left == 0) {
-          seg.next();
-          s_left = seg.n;
-          ok = wait_spin_warp(q_full, ns & 1, abort_flag, p.err);
-          ++ns;
-        }
+    int n_seg = 0, left = 0;        // segments begun; tiles left in the current one
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      const bool first = left == 0;
+      if (first) {
+        seg.next();
+        left = seg.n;
+        // the segment's Q is there; O of the segment before has been read
+        if (is_s)
+          ok = wait_spin_warp(q_full, n_seg & 1, abort_flag, p.err);
+        else if (n_seg > 0)
+          ok = wait_spin_warp(o_free, (n_seg - 1) & 1, abort_flag, p.err);
+        ++n_seg;
+      }
+      const uint32_t t_s = tmem + (uint32_t)BN * (i & 1);
+      if (is_s) {
         if (ok) ok = wait_spin_warp(&k_full[i % KST], (i / KST) & 1, abort_flag, p.err);
+        // P of tile i - 2 lies in this S buffer until its product is done
+        if (ok && i >= 2) ok = wait_spin_warp(&pv_done[i & 1], ((i >> 1) - 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
-        --s_left;
+        --left;
         if (elect_one()) {
-          issue_s<HD>(tmem + (uint32_t)BN * (i & 1), sq, sk + (i % KST) * C::KTILE, id_s);
+          issue_s<HD>(t_s, sq, sk + (i % KST) * C::KTILE, id_s);
           mma_commit(&s_full[i & 1]);
           mma_commit(&k_empty[i % KST]);
-          if (s_left == 0) mma_commit(q_empty);
+          if (left == 0) mma_commit(q_empty);
         }
         __syncwarp();
-      }
-      if (i > 0) {
-        const int t = i - 1;
-        bool first = false;
-        if (pv_left == 0) {
-          sp.next();
-          pv_left = sp.n;
-          first = true;
-          if (np > 0) ok = wait_spin_warp(o_free, (np - 1) & 1, abort_flag, p.err);   // O of the last segment read
-          ++np;
-        }
-        if (ok) ok = wait_spin_warp(&p_ready[t & 1], (t >> 1) & 1, abort_flag, p.err);
-        if (ok) ok = wait_spin_warp(&v_full[t % VST], (t / VST) & 1, abort_flag, p.err);
+      } else {
+        // a whole tile is one run of MMAs; the last tile's product stops behind its last key
+        const int ksteps = (tile_keys(seg.t0 + seg.n - left, s_len[seg.b], s_new[seg.b]) + 15) / 16;
+        const uint32_t v0 = sv + (i % VST) * C::KTILE;
+        if (ok) ok = wait_spin_warp(&v_full[i % VST], (i / VST) & 1, abort_flag, p.err);
+        if (ok) ok = wait_spin_warp(&p_ready[i & 1], (i >> 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
-        // a whole tile is one run of MMAs; the last tile's product stops behind its last key
-        const int ksteps = (tile_keys(sp.t0 + sp.n - pv_left, s_len[sp.b], s_new[sp.b]) + 15) / 16;
-        const uint32_t d_o = tmem + TM_O, tp = tmem + (uint32_t)BN * (t & 1), v0 = sv + (t % VST) * C::KTILE;
-        --pv_left;
+        --left;
         if (elect_one()) {
           if (ksteps == BN / 16) {
-            issue_pv<BN / 16>(d_o, tp, v0, id_pv, first);
+            issue_pv<BN / 16>(tmem + TM_O, t_s, v0, id_pv, first);
           } else {
 #pragma unroll 1
-            for (int kk = 0; kk < ksteps; ++kk) issue_pv<1>(d_o, tp + kk * 8, v0 + kk * 2048, id_pv, first && kk == 0);
+            for (int kk = 0; kk < ksteps; ++kk)
+              issue_pv<1>(tmem + TM_O, t_s + kk * 8, v0 + kk * 2048, id_pv, first && kk == 0);
           }
-          mma_commit(pv_done);
-          mma_commit(&v_empty[t % VST]);
-          if (pv_left == 0) mma_commit(o_full);
+          mma_commit(&pv_done[i & 1]);
+          mma_commit(&v_empty[i % VST]);
+          if (left == 0) mma_commit(o_full);
         }
         __syncwarp();
       }
@@ -552,9 +551,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       report_error(p.err, (K_TREE << 8) | SITE_MMA);
       *abort_flag = 1;
     }
-    if (elect_one()) mma_commit(drain);
+    if (elect_one()) mma_commit(&drain[is_s ? 0 : 1]);
     __syncwarp();
-    if (!wait_drain(drain, 0) && lane == 0) report_error(p.err, (K_TREE << 8) | SITE_DRAIN);
+    if (!wait_drain(&drain[is_s ? 0 : 1], 0) && lane == 0) report_error(p.err, (K_TREE << 8) | SITE_DRAIN);
     __syncwarp();
   } else if (!skip && warp < n_act) {
     // ---------------- softmax: thread = query row ----------------
@@ -600,8 +599,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           lo = (uint32_t)vis;
           hi = (uint32_t)(vis >> 32);
           // V(i): only now, behind the wait for S(i).  That was issued after the product that read
-          // the slot's last tile, so the slot's barrier is at most one phase back; before, it might
-          // be two, and a wait by parity would take the older phase for this one.
+          // the slot's last tile, so the slot's barrier is in this tile's phase; before, it might
+          // be in the last tile's, and a wait by parity would take the phase before that for this one.
           ok = wait_warp(&v_full[i % VST], (i / VST) & 1, abort_flag, p.err);
           if (!ok) break;
           clean_v<HD, FP16>(smem + C::OFF_V + (i % VST) * C::KTILE, keep, draft, bad_rows + 2 * (draft ? t - ct : 0),
@@ -639,7 +638,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         l_run += edge ? p_row<FP16, true>(s0, lo, hi, sl2, -m_run, t_s) : p_row<FP16, false>(s0, lo, hi, sl2, -m_run, t_s);
         if (rescale && t > seg.t0) {
           // O was last written by the previous tile's product: wait for it, then scale the row
-          ok = wait_warp(pv_done, (i - 1) & 1, abort_flag, p.err);
+          ok = wait_warp(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -749,7 +748,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == WARP_MMA) {
+  if (warp == WARP_S) {
     tc_fence_after();
     tmem_dealloc(tmem, TM_COLS);
   }
