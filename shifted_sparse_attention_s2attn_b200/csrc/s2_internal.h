@@ -138,7 +138,6 @@ cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* part, int n_sm, c
 constexpr int kTreeMaxM = 128;
 constexpr int kTreeMaxB = 1024;           // lengths held in shared memory
 constexpr int kTreeSlots = 2 * 148;       // two CTAs on each SM of a B200
-constexpr int kTreeMinRunLog2 = 1;        // a run has at least two key tiles
 struct TreePlan {
   int group;      // query heads of a key head
   int tok;        // drafted tokens of a 128-row tile

@@ -49,6 +49,7 @@ constexpr int BM = 128, BN = 64;
 constexpr int KST = 2, VST = 2;              // ring stages
 constexpr int NTHREADS = 256;
 constexpr int WARP_K = 4, WARP_V = 5, WARP_S = 6, WARP_PV = 7;
+static_assert(NTHREADS == 32 * (WARP_PV + 1), "four softmax warps, then these");
 constexpr uint32_t QBOX = BM * 128;          // 128 rows x 128 B (64 columns)
 constexpr uint32_t KBOX = BN * 128;
 constexpr int NBARS = 2 + 2 * KST + 2 * VST + 3 * 2 + 3 + 2;
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   uint64_t* drain = s_full + 9;         // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  int* run = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);        // sequence, tile, tiles, runs in use
+  int* run = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);        // first sequence, its first tile, tiles
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 32);  // [3][4]: drafted rows with inf/NaN
   int* s_len = reinterpret_cast<int*>(smem + C::OFF_LEN);
   int* s_new = s_len + kTreeMaxB;
@@ -330,40 +331,37 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   }
   // lengths, clamped to what the tables can hold
   const int cap = cap_tokens(p);
+  auto cached_len = [&](int b) { return min(max(p.len[b], 0), cap); };
+  auto drafted = [&](int b) { return p.new_len ? min(max(p.new_len[b], 0), p.M) : p.M; };
   for (int b = threadIdx.x; b < p.B; b += NTHREADS) {
-    const int l = p.len[b], nw = p.new_len ? p.new_len[b] : p.M;
-    const int lc = min(max(l, 0), cap), nc = min(max(nw, 0), p.M);
-    if (lc != l || nc != nw) report_error(p.index_err, (K_TREE << 8) | SITE_INDEX);
-    s_len[b] = lc;
-    s_new[b] = nc;
+    s_len[b] = cached_len(b);
+    s_new[b] = drafted(b);
+    if (s_len[b] != p.len[b] || (p.new_len && s_new[b] != p.new_len[b]))
+      report_error(p.index_err, (K_TREE << 8) | SITE_INDEX);
   }
   if (warp == WARP_S) {
     tmem_alloc(tmem_slot, TM_COLS);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  if (warp == 0) {
+  if (warp == 0) {     // (from the lengths in global memory: one barrier for all of the set-up)
     // This CTA's run.  A sequence weighs its tiles and kSeqCost more: what its end costs (masked
     // tiles, the output, the next Q).  The run takes the tiles of an equal share of the weights.
     int sum = 0, weight = 0;       // the host has checked that these fit
     for (int b = lane; b < p.B; b += 32) {
-      const int n = all_tiles(s_len[b], s_new[b], first_tok);
+      const int n = all_tiles(cached_len(b), drafted(b), first_tok);
       sum += n;
       weight += n ? n + kSeqCost : 0;
     }
     sum = __reduce_add_sync(0xffffffffu, sum);
     weight = __reduce_add_sync(0xffffffffu, weight);
-    const int runs = min(p.J, max(1, sum >> kTreeMinRunLog2));
+    const int runs = min(p.J, max(1, sum));
     const int each = weight / runs, more = weight - each * runs;   // the first `more` shares are one larger
     const int w0 = each * j + min(j, more), w1 = w0 + each + (j < more ? 1 : 0);
     // the sequence and tile that w0 falls on, and the tiles before w0 and w1
     int b0 = 0, t0 = 0, at0 = -1, at1 = -1, tiles_before = 0, weight_before = 0;
     for (int base = 0; base < p.B && j < runs; base += 32) {
       const int b = base + lane;
-      const int n = b < p.B ? all_tiles(s_len[b], s_new[b], first_tok) : 0;
+      const int n = b < p.B ? all_tiles(cached_len(b), drafted(b), first_tok) : 0;
       int ti = n, wi = n ? n + kSeqCost : 0;      // inclusive sums over the lanes
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -395,10 +393,12 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       run[0] = b0;
       run[1] = t0;
       run[2] = j < runs ? at1 - at0 : 0;
-      run[3] = runs;
     }
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   const int n_tiles = run[2];
   const bool skip = *abort_flag != 0 || n_tiles == 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
