@@ -877,9 +877,10 @@ cudaError_t launch(const TreeMaps& t, const Params& p, cudaStream_t st) {
 
 }  // namespace tree
 
-// Row tiles and runs.  A unit's J CTAs should fill whole waves of two CTAs an SM: the J up to
-// two waves' worth with the least ceil(U * J / slots) / J (the time of a unit's share times
-// the waves it takes), the smaller one on a tie, since each run more costs partials.
+// Row tiles and runs.  A unit's J CTAs should fill one wave of two CTAs an SM, or two where one
+// cannot be filled well: the J with the least waves / J (the time of a unit's share times the
+// waves), a second wave counted a fifth more for its start and its partials (16 to 32k tokens:
+// 50 units, one wave of 250 CTAs 79 us, two of 550 83; 100 units, 200 CTAs 159 us, 500 149).
 TreePlan tree_plan(int M, int H, int Hkv) {
   TreePlan t;
   t.group = H / Hkv;
@@ -890,7 +891,7 @@ TreePlan tree_plan(int M, int H, int Hkv) {
   t.J = 1;
   double best = 1e30;
   for (int J = 1; J == 1 || U * J <= 2 * kTreeSlots; ++J) {
-    const double cost = (double)((U * J + kTreeSlots - 1) / kTreeSlots) / J;
+    const double cost = (U * J <= kTreeSlots ? 1.0 : 1.2 * (double)((U * J + kTreeSlots - 1) / kTreeSlots)) / J;
     if (cost < best - 1e-9) {
       best = cost;
       t.J = J;
