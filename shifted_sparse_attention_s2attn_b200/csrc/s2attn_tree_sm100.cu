@@ -141,10 +141,11 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool wait_spin_warp(uint64_t* bar, uint32_t parity, volatile int* abort, const int* gerr) {
   return __all_sync(0xffffffffu, wait_spin(bar, parity, abort, gerr));
 }
-// Columns [4 * piece, 4 * piece + 4) of row r of a partial.
+// Columns [4 * piece, 4 * piece + 4) of row r of a partial (partials exist where a unit has several
+// runs, of which the plan makes at most two waves: their pieces fit 32 bits).
 template <int HD>
-__device__ __forceinline__ float4* part_at(const Params& p, size_t slot, int piece, int r) {
-  return reinterpret_cast<float4*>(p.part_o) + (slot * (HD / 4) + piece) * p.slot_rows + r;
+__device__ __forceinline__ float4* part_at(const Params& p, int slot, int piece, int r) {
+  return reinterpret_cast<float4*>(p.part_o) + ((slot * (HD / 4) + piece) * p.slot_rows + r);
 }
 // True in one lane of the warp.
 __device__ __forceinline__ bool elect_one() {
@@ -671,7 +672,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         ++n_draft;
       }
       const bool whole = seg.t0 == 0 && seg.n == seg.total;
-      const size_t slot = (size_t)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0), part = slot * p.slot_rows + r;
+      const int slot = (int)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0);
+      const size_t part = (size_t)slot * p.slot_rows + r;
       const size_t orow = ((size_t)b * p.M + m) * p.H + h;
       const bool st_ok =
           row_ok && (whole ? in_bounds(orow, 1, (size_t)p.B * p.M * p.H, p.err, (K_TREE << 8) | SITE_STORE)
@@ -788,7 +790,8 @@ __global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_cons
   // launched as a programmatic dependent of the attention kernel: wait for that whole grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int nw = p.new_len ? min(p.new_len[b], p.M) : p.M;
-  if (nw <= rt * p.tok || *(volatile int*)p.err != 0) return;   // the same for the whole block
+  // (the same for the whole block) no row of it exists, or an error ended the attention kernel
+  if (nw <= rt * p.tok + grp * rp / p.group || *(volatile int*)p.err != 0) return;
   const int2 fl = *reinterpret_cast<const int2*>(p.meta + (b * p.RT + rt) * 2);
   const int first = max(fl.x, 0), last = min(fl.y, p.J - 1);
   if (first >= last) return;
@@ -802,15 +805,16 @@ __global__ void __launch_bounds__(CW * 32) tree_combine_kernel(const __grid_cons
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
       const int s = s0 + k * parts;
-      ml[k] = make_float2(-INFINITY, 0.f);
-      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s > last) continue;
-      const size_t slot = ((size_t)s * U + u) * 2 + (s == first ? 1 : 0);
-      ml[k] = *reinterpret_cast<const float2*>(p.part_ml + (slot * p.slot_rows + r) * 2);
+      if (s > last) break;
+      const int slot = (s * U + u) * 2 + (s == first ? 1 : 0);
+      ml[k] = reinterpret_cast<const float2*>(p.part_ml)[slot * p.slot_rows + r];
       v[k] = *part_at<HD>(p, slot, piece, r);
     }
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) join(a, ml[k].x, ml[k].y, v[k]);
+    for (int k = 0; k < AHEAD; ++k) {
+      if (s0 + k * parts > last) break;
+      join(a, ml[k].x, ml[k].y, v[k]);
+    }
   }
   __syncwarp();
   for (int o = rp; o < 32; o <<= 1) {     // the lanes that hold the same row
