@@ -284,7 +284,8 @@ int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, i
  * and B * table_width * page_size < 2^35 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
  * aligned, at least s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the GPU
  * need one each.  Lengths are read on the device only, so a captured call follows them.  Runs
- * up to two kernels on `stream`.  The result does not depend on what else runs.
+ * up to two kernels on `stream`.  Repeated calls give the same bits; the lengths of a batch decide where
+ * a sequence's keys are cut, so its last bits may differ between batches.
  */
 size_t s2attn_tree_decode_workspace_bytes(int B, int M, int H, int Hkv, int D);
 int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, const void* k_pages,

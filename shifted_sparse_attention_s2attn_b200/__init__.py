@@ -481,8 +481,8 @@ def _norm_rope_ref(q, k, names, norm, wq, wk, inv_freq, positions, pos0):
     if ref is None:
         raise ValueError(f"{names[0]} or {names[1]} must be given")
     shape, dtype, dev = ref.shape, ref.dtype, ref.get_device()
-    if len(shape) != 4:
-        raise ValueError(f"{names[0]} and {names[1]} must be [B,N,H,D]")
+    if len(shape) != 4 or shape[0] * shape[1] >= 2 ** 30:      # (the C call's sizes are 32-bit)
+        raise ValueError(f"{names[0]} and {names[1]} must be [B,N,H,D] with B*N below 2^30")
     if wq is not None:
         _fit(wq, "wq", shape[3:], dtype, dev)
     if wk is not None:
@@ -600,6 +600,8 @@ def _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype, dev):
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_pages must be [n_pages,page_size,Hkv,D] and page_table [B,table_width]")
     n_pages, page_size, _, _ = k_pages.shape
+    if n_pages * page_size >= 2 ** 31 or page_table.shape[1] >= 2 ** 31:
+        raise ValueError("a pool must have fewer than 2^31 rows")
     shape = (n_pages, page_size, Hkv, D)
     _fit(k_pages, "k_pages", shape, dtype, dev)
     _fit(v_pages, "v_pages", shape, dtype, dev)
@@ -648,6 +650,8 @@ def s2attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, r
     if k_new.dim() != 4:
         raise ValueError("k_new must be [B,M,Hkv,D]")
     B, M, Hkv, D = k_new.shape
+    if B * M >= 2 ** 30:
+        raise ValueError("k_new must have fewer than 2^30 rows")
     dtype, dev = k_new.dtype, k_new.get_device()
     _dtype_code(dtype, "k_new", True)
     _fit(k_new, "k_new", (B, M, Hkv, D), dtype, dev)
@@ -674,8 +678,8 @@ def s2attn_cache_copy_pages(pools, pairs, stream=None):
         raise ValueError("pools must be a non-empty list")
     ref = pools[0]
     shape, dtype, dev = ref.shape, ref.dtype, ref.get_device()
-    if len(shape) < 2:
-        raise ValueError("a pool must be [n_pages, ...]")
+    if len(shape) < 2 or shape[0] >= 2 ** 31:
+        raise ValueError("a pool must be [n_pages, ...] with fewer than 2^31 pages")
     for t in pools:
         if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
             _fit(t, "every pool", shape, dtype, dev)

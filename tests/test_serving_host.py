@@ -254,3 +254,18 @@ def test_append_binding_refusals():
                      ((kn, kn, pages, pages, table, n), dict(n_rows=torch.zeros(3, dtype=torch.int32)))]:
         with pytest.raises(ValueError):
             s2.s2attn_cache_append(*args, **kw)
+
+
+def test_sizes_that_do_not_fit_the_c_call_are_refused():
+    """Expanded host tensors (no memory): sizes past 32 bits never reach a 32-bit argument."""
+    big = torch.zeros(1).expand(2 ** 20, 2 ** 12, 1, 16)
+    with pytest.raises(ValueError, match="2\\^30"):
+        s2.qk_norm_rope_fwd(big, None, big, None, torch.zeros(8))
+    with pytest.raises(ValueError, match="2\\^31"):
+        s2.s2attn_cache_copy_pages([torch.zeros(1).expand(2 ** 32 + 2, 16)], [(0, 1)])
+    with pytest.raises(ValueError, match="2\\^30"):
+        s2.s2attn_cache_append(big, big, big, big, None, None)
+    pool = torch.zeros(1).expand(2 ** 30, 16, 1, 16)
+    kn = torch.zeros(1, 1, 1, 16)
+    with pytest.raises(ValueError, match="2\\^31"):
+        s2.s2attn_cache_append(kn, kn, pool, pool, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
