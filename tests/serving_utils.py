@@ -64,7 +64,7 @@ def norm_rope_grad(x, w, dy, pos, inv_freq, norm, eps, af, interleaved):
     x = x.double()
     r = 1.0 / torch.sqrt(x.square().mean(-1, keepdim=True) + eps)
     xhat = x * r
-    wd = torch.ones(D, dtype=torch.float64) if w is None else w.double()
+    wd = torch.ones(D, dtype=torch.float64, device=dy.device) if w is None else w.double()
     gx = g * wd
     dx = r * (gx - xhat * (gx * xhat).mean(-1, keepdim=True))
     scale = r * (gs * wd.abs() + xhat.abs() * (gs * wd.abs() * xhat.abs()).mean(-1, keepdim=True))
