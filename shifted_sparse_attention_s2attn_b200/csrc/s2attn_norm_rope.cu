@@ -22,8 +22,7 @@
 // rows' threads in a fixed order and writes one partial; a second kernel adds the partials
 // in order, so dw does not depend on which CTA ran first.
 // Measured (B200, bf16, D = 128): forward of a 32k prompt, 32 + 32 heads, 183 us = 5.9 TB/s, 0.90 of
-// the copy bandwidth; forward and backward at 8k, 32 + 8 heads, 90 us (ncu: 29 and 56, the sum of
-// dw 6 alone), 4.7 TB/s.  Tried and slower: rows through a ring of bulk copies in shared memory (192
+// the copy bandwidth; forward and backward at 8k, 32 + 8 heads, 85 us, 4.9 TB/s.  Tried and slower: rows through a ring of bulk copies in shared memory (192
 // and 127 us), one chunk a lane with the other half shuffled (237 and 125), kernels of their own for
 // each layout and with or without the norm (181 and 90: nothing).
 #include <cuda_bf16.h>
@@ -41,6 +40,7 @@ constexpr int THREADS = 256;
 // CTAs an SM, all resident at once (a 32k prompt, 32 + 32 heads: 3 183 us, 2 215, 4 (64 registers,
 // spills) 201; 8k forward and backward, 32 + 8 heads: backward at 2 90 us, at 3 (spills) 118)
 constexpr int FWD_CTAS = 3, BWD_CTAS = 2;
+constexpr double kAngleRows = 3.0;   // a token's angles cost as much as this many rows (R = D)
 constexpr int MAX_TAB = 2048;   // (cos, sin) pairs of a tile, at most: 16 KB
 
 struct Side {                   // q or k
@@ -221,21 +221,24 @@ __global__ void __launch_bounds__(THREADS, BWD ? BWD_CTAS : FWD_CTAS) norm_rope_
       load_raw(yb, dy + apart);
     }
   };
+  // a thread's angles: one frequency (in turns: 1 / 2 pi), every ang_step-th token of a tile
+  const int ang_step = half ? THREADS / half : 1, ang_f = half ? (int)threadIdx.x % half : 0;
+  const int ang_tok = half && (int)threadIdx.x < ang_step * half ? (int)threadIdx.x / half : p.tile;
+  const int ang_at = tab_pos(ang_f, R, p.interleaved);
+  const double turn_freq = half ? (double)p.inv_freq[ang_f] * 0.15915494309189533577 : 0.0;
   // this CTA's tokens, an equal share
   const int tok_begin = (int)((long long)p.tokens * cta / ctas);
   const int tok_end = (int)((long long)p.tokens * (cta + 1) / ctas);
   for (int tok0 = tok_begin; tok0 < tok_end; tok0 += p.tile) {
     const int n_tok = min(p.tile, tok_end - tok0);
     __syncthreads();
-    for (int i = threadIdx.x; i < n_tok * half; i += THREADS) {
-      const int tk = i / half, f = i - tk * half;
+    for (int tk = ang_tok; tk < n_tok; tk += ang_step) {
       const int pos = p.pos ? p.pos[tok0 + tk] : p.pos0 + (tok0 + tk) % p.N;
-      const double turns = (double)pos * (double)p.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
+      const double turns = (double)pos * turn_freq;
       float sn, cn;
       sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
-      const int at = tk * half + tab_pos(f, R, p.interleaved);
-      cos_tab[at] = cn * p.af;
-      sin_tab[at] = sn * p.af;
+      cos_tab[tk * half + ang_at] = cn * p.af;
+      sin_tab[tk * half + ang_at] = sn * p.af;
     }
     __syncthreads();
 #pragma unroll 1
@@ -271,51 +274,57 @@ __global__ void __launch_bounds__(THREADS, BWD ? BWD_CTAS : FWD_CTAS) norm_rope_
         x += step;
         dy += step;
         if (has && r + ROWS < n_rows) fetch(x, dy);
-        float rstd = 1.0f;
-        if (p.norm) {
-          float2 ss = both(0.0f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ss = __ffma2_rn(a[e], a[e], __ffma2_rn(b[e], b[e], ss));
-          rstd = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_d + p.eps);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {   // xhat
-            a[e] = __fmul2_rn(a[e], both(rstd));
-            b[e] = __fmul2_rn(b[e], both(rstd));
-          }
-        }
-        if (!BWD && p.norm) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] = __fmul2_rn(a[e], w0[e]);
-            b[e] = __fmul2_rn(b[e], w1[e]);
-          }
-        }
-        if (rot && live) {
+        auto turn_row = [&](float2 (&u)[4], float2 (&v)[4]) {
+          if (!rot || !live) return;
           const int tk = s.H == 1 ? r : (int)__umulhi((uint32_t)r, s.inv_h);
           Angles g;
           get_angles(g, cos_tab + tk * half, sin_tab + tk * half, c0, c1, R, p.interleaved);
-          if (BWD)
-            turn<true>(ga, gb, g, p.interleaved);
-          else
-            turn<false>(a, b, g, p.interleaved);
-        }
-        if (BWD && p.norm) {
-          float2 dot2 = both(0.0f);
+          turn<BWD>(u, v, g, p.interleaved);
+        };
+        if (!BWD) {
+          if (p.norm) {
+            float2 ss = both(0.0f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (live) {     // behind its last row a lane holds that row's values still
-              dw0[e] = __ffma2_rn(ga[e], a[e], dw0[e]);
-              dw1[e] = __ffma2_rn(gb[e], b[e], dw1[e]);
+            for (int e = 0; e < 4; ++e) ss = __ffma2_rn(a[e], a[e], __ffma2_rn(b[e], b[e], ss));
+            const float rstd = rsqrtf(row_sum<LPR>(ss.x + ss.y) * inv_d + p.eps);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[e] = __fmul2_rn(__fmul2_rn(a[e], both(rstd)), w0[e]);
+              b[e] = __fmul2_rn(__fmul2_rn(b[e], both(rstd)), w1[e]);
             }
-            ga[e] = __fmul2_rn(ga[e], w0[e]);
-            gb[e] = __fmul2_rn(gb[e], w1[e]);
-            dot2 = __ffma2_rn(ga[e], a[e], __ffma2_rn(gb[e], b[e], dot2));
           }
-          const float dot = row_sum<LPR>(dot2.x + dot2.y) * inv_d;
+          turn_row(a, b);
+        } else {
+          turn_row(ga, gb);
+          if (p.norm) {
+            // both sums at once: of x^2, and of gx x (mean(gx xhat) is the latter times rstd / D)
+            float2 ss = both(0.0f), gs = both(0.0f);
+            float2 ha[4], hb[4];   // gx
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ga[e] = __fmul2_rn(both(rstd), __ffma2_rn(a[e], both(-dot), ga[e]));
-            gb[e] = __fmul2_rn(both(rstd), __ffma2_rn(b[e], both(-dot), gb[e]));
+            for (int e = 0; e < 4; ++e) {
+              ha[e] = __fmul2_rn(ga[e], w0[e]);
+              hb[e] = __fmul2_rn(gb[e], w1[e]);
+              ss = __ffma2_rn(a[e], a[e], __ffma2_rn(b[e], b[e], ss));
+              gs = __ffma2_rn(ha[e], a[e], __ffma2_rn(hb[e], b[e], gs));
+            }
+            float s2x = ss.x + ss.y, sgx = gs.x + gs.y;
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) {
+              s2x += __shfl_xor_sync(0xffffffffu, s2x, o);
+              sgx += __shfl_xor_sync(0xffffffffu, sgx, o);
+            }
+            const float rstd = rsqrtf(s2x * inv_d + p.eps);
+            const float dot = rstd * sgx * inv_d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 xa_hat = __fmul2_rn(a[e], both(rstd)), xb_hat = __fmul2_rn(b[e], both(rstd));
+              if (live) {     // behind its last row a lane holds that row's values still
+                dw0[e] = __ffma2_rn(ga[e], xa_hat, dw0[e]);
+                dw1[e] = __ffma2_rn(gb[e], xb_hat, dw1[e]);
+              }
+              ga[e] = __fmul2_rn(both(rstd), __ffma2_rn(xa_hat, both(-dot), ha[e]));
+              gb[e] = __fmul2_rn(both(rstd), __ffma2_rn(xb_hat, both(-dot), hb[e]));
+            }
           }
         }
         if (live) {
@@ -440,10 +449,15 @@ cudaError_t launch_norm_rope_fwd(const NormRopeArgs& a, int n_sm, cudaStream_t s
 
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* part, int n_sm, cudaStream_t st) {
   nr::Params p = nr::make(a);
-  const long long heads = p.s[0].H + p.s[1].H, most = std::min(kNormRopePartials, nr::BWD_CTAS * n_sm);
+  // a side's share of the CTAs goes by its work, rows and angles (8k, 32 + 8 heads, forward and
+  // backward: shares by rows alone 90 us, these 85)
+  const long long most = std::min(kNormRopePartials, nr::BWD_CTAS * n_sm);
+  double cost[2];
+  for (int i = 0; i < 2; ++i) cost[i] = p.s[i].H ? p.s[i].H + nr::kAngleRows * p.R / p.D : 0.0;
   int ctas[2];
   for (int i = 0; i < 2; ++i)
-    ctas[i] = p.s[i].H ? nr::ctas_for(p, p.s[i].H, 2 * n_sm * p.s[i].H / heads, std::max(1LL, most * p.s[i].H / heads)) : 0;
+    ctas[i] = p.s[i].H ? nr::ctas_for(p, p.s[i].H, (long long)(2 * n_sm * cost[i] / (cost[0] + cost[1])),
+                                      std::max(1LL, (long long)(most * cost[i] / (cost[0] + cost[1])))) : 0;
   p.ctas_q = ctas[0];
   p.tile = nr::tile_for(p, ctas[0] && ctas[1] ? std::min(ctas[0], ctas[1]) : ctas[0] + ctas[1]);
   if (a.dwq && p.s[0].H) p.s[0].part = part;
