@@ -280,22 +280,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Wait of the MMA-issuing thread: polls the barrier with test_wait instead of suspending in
-// try_wait, checking the abort flags and the time limit every 1024 polls.  In the decoding step it is 1.5-2.5 %
-// faster at every M (the softmax warps' arrival is seen sooner); in the attention forward and
-// backward, whose MMA thread shares its SM sub-partition with busy warps, polling was slower.
-__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort, const int* gerr) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_test_wait(bar, parity)) return true;
-    if ((n & 1023u) == 0) {
-      if (*abort || *(const volatile int*)gerr) return false;
-      if (globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
-    }
-  }
-}
-
 // Elementwise product of two bf16x2 words, rounded to bf16 (nearest even).  Runs on the
 // half-precision pipe: fp32 FFMA/FMUL at a high rate slow concurrent tcgen05 MMAs on the
 // same SM (measured: 64 -> 130-160 cycles per 128x128x16 MMA), bf16x2 arithmetic does not.

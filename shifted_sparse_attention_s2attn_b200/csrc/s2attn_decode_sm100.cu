@@ -427,6 +427,23 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const Par
 // layout as above.
 namespace dtc {
 
+// Wait of the MMA-issuing thread: polls the barrier with test_wait instead of suspending in
+// try_wait, checking the abort flags and the time limit every 1024 polls.  Here it is 1.5-2.5 %
+// faster at every M (the softmax warps' arrival is seen sooner); in the attention forward and
+// backward, whose MMA thread shares its SM sub-partition with busy warps, polling was slower.
+__device__ __forceinline__ bool wait_spin(uint64_t* bar, uint32_t parity, volatile int* abort, const int* gerr) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if ((n & 1023u) == 0) {
+      if (*abort || *(const volatile int*)gerr) return false;
+      if (globaltimer_ns() - t0 > kWaitTimeoutNs) return false;
+    }
+  }
+}
+
+
 constexpr int HD = 128, BM = 128, BN = kDecodeTileKeys;  // 64 keys per tile
 constexpr uint32_t QBOX = BM * 128;           // 128 rows x 128 B (64 bf16 columns)
 constexpr uint32_t KBOX = BN * 128;           // 64 rows x 128 B

@@ -22,9 +22,10 @@
 // rows' threads in a fixed order and writes one partial; a second kernel adds the partials
 // in order, so dw does not depend on which CTA ran first.
 // Measured (B200, bf16, D = 128): forward of a 32k prompt, 32 + 32 heads, 183 us = 5.9 TB/s, 0.90 of
-// the copy bandwidth; forward and backward at 8k, 32 + 8 heads, 85 us, 4.9 TB/s.  Tried and slower: rows through a ring of bulk copies in shared memory (192
-// and 127 us), one chunk a lane with the other half shuffled (237 and 125), kernels of their own for
-// each layout and with or without the norm (181 and 90: nothing).
+// the copy bandwidth; forward and backward at 8k, 32 + 8 heads, 85 us, 4.9 TB/s.  Tried and not
+// kept: rows through a ring of bulk copies in shared memory (192 and 127 us), one chunk a lane with
+// the other half shuffled (237 and 125), kernels of their own for each layout and for rows with and
+// without the norm (181 and 90).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

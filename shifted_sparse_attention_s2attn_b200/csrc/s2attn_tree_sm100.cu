@@ -150,9 +150,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, gerr));
 }
 
-__device__ __forceinline__ bool wait_spin_warp(uint64_t* bar, uint32_t parity, volatile int* abort, const int* gerr) {
-  return __all_sync(0xffffffffu, wait_spin(bar, parity, abort, gerr));
-}
 // Columns [4 * piece, 4 * piece + 4) of row r of a partial (partials exist where a unit has several
 // runs, of which the plan makes at most two waves: their pieces fit 32 bits).
 template <int HD>
@@ -516,16 +513,16 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         left = seg.n;
         // the segment's Q is there; O of the segment before has been read
         if (is_s)
-          ok = wait_spin_warp(q_full, n_seg & 1, abort_flag, p.err);
+          ok = wait_warp(q_full, n_seg & 1, abort_flag, p.err);
         else if (n_seg > 0)
-          ok = wait_spin_warp(o_free, (n_seg - 1) & 1, abort_flag, p.err);
+          ok = wait_warp(o_free, (n_seg - 1) & 1, abort_flag, p.err);
         ++n_seg;
       }
       const uint32_t t_s = tmem + (uint32_t)BN * (i & 1);
       if (is_s) {
-        if (ok) ok = wait_spin_warp(&k_full[i % KST], (i / KST) & 1, abort_flag, p.err);
+        if (ok) ok = wait_warp(&k_full[i % KST], (i / KST) & 1, abort_flag, p.err);
         // P of tile i - 2 lies in this S buffer until its product is done
-        if (ok && i >= 2) ok = wait_spin_warp(&pv_done[i & 1], ((i >> 1) - 1) & 1, abort_flag, p.err);
+        if (ok && i >= 2) ok = wait_warp(&pv_done[i & 1], ((i >> 1) - 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
         --left;
@@ -540,8 +537,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         // a whole tile is one run of MMAs; the last tile's product stops behind its last key
         const int ksteps = (tile_keys(seg.t0 + seg.n - left, s_len[seg.b], s_new[seg.b]) + 15) / 16;
         const uint32_t v0 = sv + (i % VST) * C::KTILE;
-        if (ok) ok = wait_spin_warp(&v_full[i % VST], (i / VST) & 1, abort_flag, p.err);
-        if (ok) ok = wait_spin_warp(&p_ready[i & 1], (i >> 1) & 1, abort_flag, p.err);
+        if (ok) ok = wait_warp(&v_full[i % VST], (i / VST) & 1, abort_flag, p.err);
+        if (ok) ok = wait_warp(&p_ready[i & 1], (i >> 1) & 1, abort_flag, p.err);
         if (!ok) break;
         tc_fence_after();
         --left;
