@@ -298,7 +298,7 @@ int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, cons
  * Writes rows of k_new and v_new ([B, M, Hkv, D]) into the pages of their sequences: for j < n_rows[b],
  * row rows[b][j] goes to position cache_len[b] + j.  rows [B, A] int32 (any order, repeats allowed);
  * NULL: row j, A = M.  n_rows [B] int32 (values above A count as A, below 0 as 0); NULL: A.
- * cache_len is not changed.  elem_size: bytes of an element (2 or 4); Hkv * D * elem_size must be a
+ * cache_len is not changed.  k_new and v_new must not overlap the pools.  elem_size: bytes of an element (2 or 4); Hkv * D * elem_size must be a
  * multiple of 16.  No two sequences may own the same page at a position that is written.
  */
 int s2attn_cache_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, const int* page_table,
