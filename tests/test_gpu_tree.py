@@ -354,3 +354,13 @@ def test_two_host_threads_at_once():
     no_device_error()
     for w, g in zip(want, got):
         assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
+
+
+@pytest.mark.parametrize("lens,M,H,Hkv,D,page", [
+    ([i % 37 for i in range(1024)], 1, 2, 1, 64, 16),       # the most sequences a call takes
+    ([10, 5000, 4096], 3, 6, 2, 128, 4096),                 # pages far larger than a tile
+    ([9000], 1, 1, 1, 64, 16),                              # one row, hundreds of runs of one tile
+    ([50], 1, 300, 300, 64, 16),                            # more units than CTAs fit: one run each
+])
+def test_sizes_at_the_ends(lens, M, H, Hkv, D, page):
+    _check(*_case(lens, M, H, Hkv, D, page, BF, "chain"), ragged=False)
