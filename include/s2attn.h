@@ -237,8 +237,9 @@ int qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const voi
  *   2 (a larger base): the base becomes base * factor^(R / (R - 2)).
  *   3 (by wavelength): frequencies that turn more than beta_fast times within original_len
  *     tokens stay, those below beta_slow are divided by factor, with a linear ramp over i
- *     between floor(i_fast) and ceil(i_slow), i_n = R ln(original_len / (2 pi n)) / (2 ln base);
- *     *attn_factor = 0.1 ln(factor) + 1.
+ *     between lo = max(0, floor(i_fast)) and hi = min(R - 1, ceil(i_slow)),
+ *     i_n = R ln(original_len / (2 pi n)) / (2 ln base) (hi <= lo: a step behind lo; hi may lie
+ *     behind the last frequency); *attn_factor = 0.1 ln(factor) + 1.
  * *attn_factor is 1 otherwise.  Requirements: R even, 2 <= R <= 256 (R >= 4 for scaling 2);
  * base > 1; factor >= 1; for scaling 3 original_len >= 1 and beta_fast > beta_slow > 0.
  */

@@ -714,7 +714,8 @@ int rope_inv_freq(float* inv_freq, float* attn_factor, int R, float base, int sc
   if (scaling == 3) {
     const double turns = R / (2 * std::log((double)base));
     low = std::max(0.0, std::floor(turns * std::log(original_len / (2 * M_PI * beta_fast))));
-    high = std::min(R / 2 - 1.0, std::ceil(turns * std::log(original_len / (2 * M_PI * beta_slow))));
+    // (may lie behind the last frequency, R/2 - 1: the ramp then ends before it has reached 1)
+    high = std::min(R - 1.0, std::ceil(turns * std::log(original_len / (2 * M_PI * beta_slow))));
   }
   for (int i = 0; i < R / 2; ++i) {
     double f = std::pow(b, -2.0 * i / R);
