@@ -279,7 +279,8 @@ int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, i
  * Token m of sequence b attends to the cache's cache_len[b] tokens and to the drafted tokens
  * j < new_len[b] whose bit is set in its mask row.  Rows m >= new_len[b] of o and lse are left as
  * they were.  A token that sees nothing gets o = 0 and lse = -inf.  What is not visible to
- * a token does not reach it, whatever it holds (infinities and NaN included).
+ * a token does not reach it, whatever it holds (infinities and NaN included).  A visible key of
+ * score -inf has weight 0; a token whose scores are all -inf gets o = 0 and lse = -inf too.
  * dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to dtype for the
  * second product.  Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024
  * and B * table_width * page_size < 2^35 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte

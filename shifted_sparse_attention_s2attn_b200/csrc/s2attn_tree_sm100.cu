@@ -638,14 +638,16 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
         // the running max moves only when it grows by more than 2^8 (P then stays below 2^8,
-        // inside fp16's range too); a row that has seen no key keeps -inf and its P stays 0
+        // inside fp16's range too); a row that has seen no score above -inf keeps -inf, and its
+        // P = exp2(-inf - 0) stays 0 (-inf - -inf is NaN)
         const float m_new = fmaxf(m_run, mx * sl2);
         const bool need = (m_new - m_run) > 8.0f;
         const bool rescale = __any_sync(0xffffffffu, need);
         const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
         if (need) m_run = m_new;
         l_run *= alpha;
-        l_run += edge ? p_row<FP16, true>(s0, lo, hi, sl2, -m_run, t_s) : p_row<FP16, false>(s0, lo, hi, sl2, -m_run, t_s);
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+        l_run += edge ? p_row<FP16, true>(s0, lo, hi, sl2, neg_m, t_s) : p_row<FP16, false>(s0, lo, hi, sl2, neg_m, t_s);
         if (rescale && t > seg.t0) {
           // O was last written by the previous tile's product: wait for it, then scale the row
           ok = wait_warp(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag, p.err);
