@@ -282,7 +282,7 @@ int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, i
  * a token does not reach it, whatever it holds (infinities and NaN included).  A visible key of
  * score -inf has weight 0; a token whose scores are all -inf gets o = 0 and lse = -inf too.
  * dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to dtype for the
- * second product.  Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024
+ * second product (in fp16 what is below 2^-36 of a row's largest weight is lost there).  Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024
  * and B * table_width * page_size < 2^35 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
  * aligned, at least s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the GPU
  * need one each.  Lengths are read on the device only, so a captured call follows them.  Runs

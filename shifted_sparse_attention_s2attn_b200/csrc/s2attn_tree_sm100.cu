@@ -39,7 +39,8 @@
 // this took 207.  Its N = 64 MMAs cost as much as N = 128 ones (A is read from shared memory at
 // each): the tensor pipe is active 55 % of the cycles.
 // P is rounded to the input's 16-bit type (the tensor cores take both operands in one type);
-// its sum is kept from the unrounded fp32 values.  Scores, maxima, sums and O are fp32.
+// its sum is kept from the unrounded fp32 values.  Scores, maxima, sums and O are fp32.  fp16
+// holds nothing below 2^-25, so P is scaled there to a largest element of 2^11 at least (kShift).
 //
 // Keys that nobody may see are never multiplied: V rows behind the last token of a tile are
 // zeroed in shared memory (0 * NaN is NaN), and a drafted V row that holds infinities or NaN
@@ -186,6 +187,19 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t tp, uint32_t sv, u
     mma_ts(d, tp + kk * 8, sdesc_add(dv, kk * 2048), idesc, (first && kk == 0) ? 0u : 1u);
 }
 
+// P = exp2(s log2(e) / sqrt(D) - m + kShift), with a running maximum m that moves only when it grows by
+// more than kLag: P stays at or below 2^(kLag + kShift), inside the type's range.  fp16 ends at
+// 2^16 and loses what is below 2^-25: shifted by 11 that is 2^-36 of the row's largest weight, and 100k keys
+// of such weights 2^-19 (unshifted, one key 17 nats ahead of 100k others took them out of o).
+// The sum and O carry the same factor; the maximum that leaves the run is m - kShift.
+// Measured in fp16 (100k cached, 64 drafted, 64 heads over 8): 220 us as unshifted with a lag of 8, and
+// as a lag of 8 with a shift of 7; with scores three times as wide, whose maximum moves more
+// often, 230 against 225, which buys 2^-36 for 2^-32.
+template <bool FP16>
+constexpr float kLag = FP16 ? 4.0f : 8.0f;
+template <bool FP16>
+constexpr float kShift = FP16 ? 11.0f : 0.0f;
+
 template <bool FP16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if (FP16) {
@@ -209,7 +223,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// P row = exp2(s * sl2 - m), zero in columns whose bit of (lo, hi) is clear (MASK), as 16-bit
+// P row = exp2(s * sl2 + neg_m), zero in columns whose bit of (lo, hi) is clear (MASK), as 16-bit
 // pairs over the first 32 columns of the row's S buffer; returns the fp32 row sum.
 template <bool FP16, bool MASK>
 __device__ __forceinline__ float p_row(const uint32_t (&sr)[64], uint32_t lo, uint32_t hi, float sl2, float neg_m,
@@ -637,16 +651,15 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         }
         const float mx = fmaxf(fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])),
                                fmaxf(fmaxf(mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7])));
-        // the running max moves only when it grows by more than 2^8 (P then stays below 2^8,
-        // inside fp16's range too); a row that has seen no score above -inf keeps -inf, and its
-        // P = exp2(-inf - 0) stays 0 (-inf - -inf is NaN)
+        // the running max moves only when it grows by more than kLag; a row that has seen no score
+        // above -inf keeps -inf, and its P = exp2(-inf - 0) stays 0 (-inf - -inf is NaN)
         const float m_new = fmaxf(m_run, mx * sl2);
-        const bool need = (m_new - m_run) > 8.0f;
+        const bool need = (m_new - m_run) > kLag<FP16>;
         const bool rescale = __any_sync(0xffffffffu, need);
         const float alpha = need ? ex2_approx(m_run - m_new) : 1.0f;
         if (need) m_run = m_new;
         l_run *= alpha;
-        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+        const float neg_m = m_run == -INFINITY ? 0.f : kShift<FP16> - m_run;
         l_run += edge ? p_row<FP16, true>(s0, lo, hi, sl2, neg_m, t_s) : p_row<FP16, false>(s0, lo, hi, sl2, neg_m, t_s);
         if (rescale && t > seg.t0) {
           // O was last written by the previous tile's product: wait for it, then scale the row
@@ -735,12 +748,13 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         }
       }
       if (st_ok) {
+        const float m_out = m_run - kShift<FP16>;
         if (whole) {
           p.lse[((size_t)b * p.H + h) * p.M + m] =
-              l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+              l_run == 0.f ? -INFINITY : (m_out + log2f(l_run)) * 0.69314718055994531f;
         } else {
           // a row all of whose scores were NaN has no maximum: 0 takes its NaN sum through the join
-          p.part_ml[part * 2] = l_run != l_run && m_run == -INFINITY ? 0.f : m_run;
+          p.part_ml[part * 2] = l_run != l_run && m_run == -INFINITY ? 0.f : m_out;
           p.part_ml[part * 2 + 1] = l_run;
         }
       }
