@@ -32,8 +32,8 @@ struct AppendArgs {
 };
 
 // Slot t = (b, j) of a block's `tpb`: its rows of k_new and v_new are found by one thread (a row
-// outside the new rows, a position outside the table or a page outside the pool is recorded
-// and skipped), then all threads copy the slots' rows.
+// outside the new rows, a negative length, a position outside the table or a page outside the
+// pool is recorded and skipped), then all threads copy the slots' rows.
 __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ long long s_src[MAX_SLOTS], s_dst[MAX_SLOTS];   // first piece of the row; -1: no row
   const long long slot0 = (long long)blockIdx.x * a.tpb;
@@ -44,9 +44,10 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
     long long src = -1, dst = -1;
     if (!a.n_rows || j < a.n_rows[b]) {
       const int row = a.rows ? a.rows[slot] : j;
-      const long long pos = (long long)a.len[b] + j, pg = pos >> a.page_shift;
+      const int len = a.len[b];
+      const long long pos = (long long)len + j, pg = pos >> a.page_shift;
       int page = -1;
-      if (row >= 0 && row < a.M && pos >= 0 && pg < a.width) page = a.table[(size_t)b * a.width + pg];
+      if (row >= 0 && row < a.M && len >= 0 && pg < a.width) page = a.table[(size_t)b * a.width + pg];
       if (page >= 0 && page < a.n_pages) {
         src = ((long long)b * a.M + row) * a.cpr;
         dst = (((long long)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1))) * a.cpr;
