@@ -190,7 +190,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t tp, uint32_t sv, u
 // P = exp2(s log2(e) / sqrt(D) - m + kShift), with a running maximum m that moves only when it grows by
 // more than kLag: P stays at or below 2^(kLag + kShift), inside the type's range.  fp16 ends at
 // 2^16 and loses what is below 2^-25: shifted by 11 that is 2^-36 of the row's largest weight, and 100k keys
-// of such weights 2^-19 (unshifted, one key 17 nats ahead of 100k others took them out of o).
+// of such weights 2^-19 (unshifted, one key 17.5 nats ahead of 100k others took them out of o).
 // The sum and O carry the same factor; the maximum that leaves the run is m - kShift.
 // Measured in fp16 (100k cached, 64 drafted, 64 heads over 8): 220 us as unshifted with a lag of 8, and
 // as a lag of 8 with a shift of 7; with scores three times as wide, whose maximum moves more
