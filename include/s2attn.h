@@ -285,7 +285,8 @@ int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, i
  * second product (in fp16 what is below 2^-36 of a row's largest weight is lost there).  Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024
  * and B * table_width * page_size < 2^35 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
  * aligned, at least s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the GPU
- * need one each.  Lengths are read on the device only, so a captured call follows them.  Runs
+ * need one each.  Lengths are read on the device only, so a captured call follows them; they
+ * must not change while it runs.  o and lse must not overlap the inputs.  Runs
  * up to two kernels on `stream`.  Repeated calls give the same bits; the lengths of a batch decide where
  * a sequence's keys are cut, so its last bits may differ between batches.
  */

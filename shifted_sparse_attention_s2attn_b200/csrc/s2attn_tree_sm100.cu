@@ -353,31 +353,43 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int i = 0; i < 12; ++i) bad[i] = 0;
     fence_mbar_init();
   }
-  // lengths, clamped to what the tables can hold
-  const int cap = cap_tokens(p);
-  auto cached_len = [&](int b) { return min(max(p.len[b], 0), cap); };
-  auto drafted = [&](int b) { return p.new_len ? min(max(p.new_len[b], 0), p.M) : p.M; };
-  for (int b = threadIdx.x; b < p.B; b += NTHREADS) {
-    s_len[b] = cached_len(b);
-    s_new[b] = drafted(b);
-    if (s_len[b] != p.len[b] || (p.new_len && s_new[b] != p.new_len[b]))
-      report_error(p.index_err, (K_TREE << 8) | SITE_INDEX);
-  }
   if (warp == WARP_S) {
     tmem_alloc(tmem_slot, TM_COLS);
     tmem_relinquish();
   }
-  if (warp == 0) {     // (from the lengths in global memory: one barrier for all of the set-up)
-    // This CTA's run.  A sequence weighs its tiles and kSeqCost more: what its end costs (masked
-    // tiles, the output, the next Q).  The run takes the tiles of an equal share of the weights.
+  if (warp == 0) {
+    // The lengths, clamped to what the tables can hold.  They are read once, eight a lane in flight, and
+    // a lane reads back only what it has stored: the run below and all segments come from the same
+    // numbers whatever becomes of the lengths meanwhile, and one barrier does for all of the set-up.
+    // A sequence weighs its tiles and kSeqCost more: what its end costs (masked tiles, the
+    // output, the next Q).
+    constexpr int AHEAD = 8;
+    const int cap = cap_tokens(p);
     int sum = 0, weight = 0;       // the host has checked that these fit
-    for (int b = lane; b < p.B; b += 32) {
-      const int n = all_tiles(cached_len(b), drafted(b), first_tok);
-      sum += n;
-      weight += n ? n + kSeqCost : 0;
+    for (int base = lane; base < p.B; base += 32 * AHEAD) {
+      int len[AHEAD], nw[AHEAD];
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+        const int b = base + 32 * e;
+        len[e] = b < p.B ? p.len[b] : 0;
+        nw[e] = b < p.B && p.new_len ? p.new_len[b] : p.M;
+      }
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+        const int b = base + 32 * e;
+        if (b >= p.B) break;
+        const int cached = min(max(len[e], 0), cap), drafted = min(max(nw[e], 0), p.M);
+        s_len[b] = cached;
+        s_new[b] = drafted;
+        if (cached != len[e] || drafted != nw[e]) report_error(p.index_err, (K_TREE << 8) | SITE_INDEX);
+        const int n = all_tiles(cached, drafted, first_tok);
+        sum += n;
+        weight += n ? n + kSeqCost : 0;
+      }
     }
     sum = __reduce_add_sync(0xffffffffu, sum);
     weight = __reduce_add_sync(0xffffffffu, weight);
+    // this CTA's run: the tiles of an equal share of the weights
     const int runs = min(p.J, max(1, sum));
     const int each = weight / runs, more = weight - each * runs;   // the first `more` shares are one larger
     const int w0 = each * j + min(j, more), w1 = w0 + each + (j < more ? 1 : 0);
@@ -385,7 +397,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     int b0 = 0, t0 = 0, at0 = -1, at1 = -1, tiles_before = 0, weight_before = 0;
     for (int base = 0; base < p.B && j < runs; base += 32) {
       const int b = base + lane;
-      const int n = b < p.B ? all_tiles(cached_len(b), drafted(b), first_tok) : 0;
+      const int n = b < p.B ? all_tiles(s_len[b], s_new[b], first_tok) : 0;
       int ti = n, wi = n ? n + kSeqCost : 0;      // inclusive sums over the lanes
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

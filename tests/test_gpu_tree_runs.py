@@ -53,3 +53,39 @@ def test_first_and_last_run_of_every_sequence(lens, new, M, H, Hkv):
             if t0 + n == total:
                 want[b][1] = j
         assert [row[rt] for row in noted] == want
+
+
+def test_lengths_that_change_while_calls_run_leave_the_next_call_right():
+    """Every block takes its run and its keys from one reading of the lengths: a call whose lengths another
+    stream changes may mix their results, but ends, and the next call is as ever."""
+    B, M, H, D, page = 40, 3, 2, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").bfloat16()
+    rng = random.Random(1)
+    lens = [torch.tensor([rng.randint(0, 2000) for _ in range(B)], dtype=torch.int32, device="cuda") for _ in range(2)]
+    news = [torch.tensor([rng.randint(0, M) for _ in range(B)], dtype=torch.int32, device="cuda") for _ in range(2)]
+    kp, vp = rnd(200, page, 1, D), rnd(200, page, 1, D)
+    table = torch.randint(0, 200, (B, 125), generator=g, device="cuda", dtype=torch.int32)
+    q, kn, vn = rnd(B, M, H, D), rnd(B, M, 1, D), rnd(B, M, 1, D)
+    n, new = lens[0].clone(), news[0].clone()
+    ws = torch.empty(s2.s2attn_tree_decode_workspace_bytes(B, M, H, 1, D), dtype=torch.uint8, device="cuda").fill_(0xff)
+
+    def call():
+        o, lse = torch.zeros_like(q), torch.zeros(B, H, M, device="cuda")
+        s2.s2attn_tree_decode(q, kn, vn, kp, vp, table, n, o, lse, ws, new_len=new)
+        return o, lse
+    want = call()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for i in range(200):
+        with torch.cuda.stream(other):
+            for j in range(4):
+                n.copy_(lens[j % 2])
+                new.copy_(news[j % 2])
+        call()
+    torch.cuda.synchronize()
+    n.copy_(lens[0])
+    new.copy_(news[0])
+    got = call()
+    no_device_error()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
