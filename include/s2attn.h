@@ -207,10 +207,10 @@ int rope_pi_apply_offset(void* q, void* k, int B, int N, int H, int D, int pos0,
  *   wq, wk   : [D] weights of dtype, NULL for 1
  *   positions: [B, N] int32, any value, or NULL: row t of every sequence is at pos0 + t
  *   inv_freq : [R/2] fp32 frequencies (device), e.g. from rope_inv_freq
- * dtype: S2ATTN_BF16, S2ATTN_FP16 or S2ATTN_F32.  Sums and products are fp32, angles are formed
- * and reduced in 64 bits, the result is rounded once.  q_out == q and k_out == k (in place) are
- * allowed; other overlaps are not.  Requirements: D % 16 == 0, D <= 256; R % 16 == 0,
- * 0 <= R <= D; Hq, Hk <= 16384; eps >= 0; device pointers 16-byte aligned (positions and inv_freq 4-byte).
+ * dtype: S2ATTN_BF16, S2ATTN_FP16 or S2ATTN_F32.  Sums and products are fp32, angles are formed and reduced in
+ * 64 bits, the result is rounded once.  q_out == q and k_out == k (in place) are allowed; other overlaps are
+ * not.  Requirements: D % 16 == 0, D <= 256; R % 16 == 0, 0 <= R <= D; Hq, Hk <= 16384; B * N < 2^30; pos0 + N
+ * < 2^31; eps >= 0; device pointers 16-byte aligned (positions and inv_freq 4-byte).
  */
 int qk_norm_rope_fwd(const void* q, const void* k, const void* wq, const void* wk, const int* positions,
                      const float* inv_freq, void* q_out, void* k_out, int B, int N, int Hq, int Hk, int D, int R,
@@ -276,19 +276,19 @@ int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, i
  *   tree_mask    : [B, M, ceil(M/64)] words as above, any bits; NULL: token m sees j <= m
  *   new_len      : [B] int32 in 0..M, or NULL for M: sequence b has new_len[b] drafted tokens
  *   o            : [B, M, H, D];  lse: [B, H, M] fp32, natural log of the sum of exp(score)
- * Token m of sequence b attends to the cache's cache_len[b] tokens and to the drafted tokens
- * j < new_len[b] whose bit is set in its mask row.  Rows m >= new_len[b] of o and lse are left as
- * they were.  A token that sees nothing gets o = 0 and lse = -inf.  What is not visible to
- * a token does not reach it, whatever it holds (infinities and NaN included).  A visible key of
- * score -inf has weight 0; a token whose scores are all -inf gets o = 0 and lse = -inf too.
- * dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to dtype for the
- * second product (in fp16 what is below 2^-36 of a row's largest weight is lost there).  Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024
- * and B * table_width * page_size < 2^35 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
- * aligned, at least s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the GPU
- * need one each.  Lengths are read on the device only, so a captured call follows them; they
- * must not change while it runs.  o and lse must not overlap the inputs.  Runs
- * up to two kernels on `stream`.  Repeated calls give the same bits; the lengths of a batch decide where
- * a sequence's keys are cut, so its last bits may differ between batches.
+ * Token m of sequence b attends to the cache's cache_len[b] tokens and to the drafted tokens j < new_len[b]
+ * whose bit is set in its mask row.  Rows m >= new_len[b] of o and lse are left as they were.  A token that
+ * sees nothing gets o = 0 and lse = -inf.  What is not visible to a token does not reach it, whatever it holds
+ * (infinities and NaN included).  A visible key of score -inf has weight 0; a token whose scores are all -inf
+ * gets o = 0 and lse = -inf too. dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to
+ * dtype for the second product (in fp16 what is below 2^-36 of a row's largest weight is lost there).
+ * Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024, B * M * H < 2^31 and B *
+ * (table_width * page_size / 64 + 16) < 2^30 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
+ * aligned, at least s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the
+ * GPU need one each.  Lengths are read on the device only, so a captured call follows them; they must not
+ * change while it runs.  o and lse must not overlap the inputs.  Runs up to two kernels on `stream`.  Repeated
+ * calls give the same bits; the lengths of a batch decide where a sequence's keys are cut, so its last bits
+ * may differ between batches.
  */
 size_t s2attn_tree_decode_workspace_bytes(int B, int M, int H, int Hkv, int D);
 int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, const void* k_pages,
@@ -298,11 +298,12 @@ int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, cons
                        size_t workspace_bytes, void* stream);
 
 /*
- * Writes rows of k_new and v_new ([B, M, Hkv, D]) into the pages of their sequences: for j < n_rows[b],
- * row rows[b][j] goes to position cache_len[b] + j.  rows [B, A] int32 (any order, repeats allowed);
- * NULL: row j, A = M.  n_rows [B] int32 (values above A count as A, below 0 as 0); NULL: A.
- * cache_len is not changed.  k_new and v_new must not overlap the pools.  elem_size: bytes of an element (2 or 4); Hkv * D * elem_size must be a
- * multiple of 16.  No two sequences may own the same page at a position that is written.
+ * Writes rows of k_new and v_new ([B, M, Hkv, D]) into the pages of their sequences: for j < n_rows[b], row
+ * rows[b][j] goes to position cache_len[b] + j.  rows [B, A] int32 (any order, repeats allowed); NULL: row j,
+ * A = M.  n_rows [B] int32 (values above A count as A, below 0 as 0); NULL: A. cache_len is not changed.
+ * k_new and v_new must not overlap the pools.  elem_size: bytes of an element (2 or 4); Hkv * D * elem_size
+ * must be a multiple of 16, at most 2^20, and B * M and B * A below 2^30 (else S2ATTN_ERR_UNSUPPORTED).  No
+ * two sequences may own the same page at a position that is written.
  */
 int s2attn_cache_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, const int* page_table,
                         const int* cache_len, const int* rows, const int* n_rows, int B, int M, int A, int Hkv, int D,
@@ -314,7 +315,7 @@ int s2attn_cache_append(const void* k_new, const void* v_new, void* k_pages, voi
  * sequence (its last, partly filled page gets a copy; full pages are shared by the tables) and
  * to move pages.  pairs is a host array, checked before anything is enqueued: pages in
  * [0, n_pages), no page written twice, none both read and written (S2ATTN_ERR_INVALID_ARG).
- * One page may be read several times.  page_bytes: bytes of a page, a multiple of 16.
+ * One page may be read several times.  page_bytes: bytes of a page, a multiple of 16, at most 2^40.
  * n_pairs = 0 does nothing.
  */
 int s2attn_cache_copy_pages(void* const* pools, int n_pools, const int* pairs, int n_pairs, int n_pages,

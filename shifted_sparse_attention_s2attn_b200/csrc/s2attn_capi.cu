@@ -758,7 +758,7 @@ int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, cons
   if (rc) return rc;
   if ((rc = check_pages(n_pages, page_size, table_width))) return rc;
   // the kernel counts key tiles of 64 (and a few more a sequence) in 32 bits
-  if ((double)B * ((double)table_width * page_size / 64 + 16) > INT_MAX / 2) return S2ATTN_ERR_UNSUPPORTED;
+  if ((double)B * ((double)table_width * page_size / 64 + 16) >= 1073741824.0) return S2ATTN_ERR_UNSUPPORTED;
   if (dtype != S2ATTN_BF16 && dtype != S2ATTN_FP16) return S2ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
       !aligned16(o) || !aligned4(lse) || !aligned4(page_table) || !aligned4(cache_len))
