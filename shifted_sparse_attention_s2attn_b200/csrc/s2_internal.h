@@ -137,7 +137,9 @@ cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, float* part, int n_sm, c
 // Attention of drafted tokens over a paged cache (s2attn_tree_sm100.cu) and their masks.
 constexpr int kTreeMaxM = 128;
 constexpr int kTreeMaxB = 1024;           // lengths held in shared memory
-constexpr int kTreeSlots = 2 * 148;       // two CTAs on each SM of a B200
+// Two CTAs on each SM of a B200.  The plan, and with it the workspace's size, follows from the shapes
+// alone and asks no device.
+constexpr int kTreeSlots = 2 * 148;
 struct TreePlan {
   int group;      // query heads of a key head
   int tok;        // drafted tokens of a 128-row tile
@@ -168,7 +170,7 @@ constexpr int kCacheMaxPools = 128;
 constexpr int kCacheCopyPairs = 448;      // page pairs of one launch
 cudaError_t launch_cache_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, const int* table,
                                 const int* len, const int* rows, const int* n_rows, int B, int M, int A, int width,
-                                int n_pages, int page_shift, int row_bytes, int* index_err, cudaStream_t st);
+                                int n_pages, int page_shift, int row_bytes, int n_sm, int* index_err, cudaStream_t st);
 cudaError_t launch_cache_copy(void* const* pools, int n_pools, const int* pairs, int n_pairs, long long page_bytes,
                               cudaStream_t st);
 

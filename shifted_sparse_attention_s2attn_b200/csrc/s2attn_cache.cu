@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kTreeMaxM) tree_mask_kernel(const int* parents
 
 cudaError_t launch_cache_append(const void* k_new, const void* v_new, void* k_pages, void* v_pages, const int* table,
                                 const int* len, const int* rows, const int* n_rows, int B, int M, int A, int width,
-                                int n_pages, int page_shift, int row_bytes, int* index_err, cudaStream_t st) {
+                                int n_pages, int page_shift, int row_bytes, int n_sm, int* index_err, cudaStream_t st) {
   cache::AppendArgs a{};
   a.k_new = static_cast<const uint4*>(k_new), a.v_new = static_cast<const uint4*>(v_new);
   a.k_pages = static_cast<uint4*>(k_pages), a.v_pages = static_cast<uint4*>(v_pages);
@@ -155,7 +155,7 @@ cudaError_t launch_cache_append(const void* k_new, const void* v_new, void* k_pa
   // one step of the block's threads, fewer slots where that leaves SMs without a block
   const int per_block = cache::THREADS * cache::UNROLL;
   const long long slots = (long long)B * A;
-  a.tpb = (int)std::max(1LL, std::min({(long long)per_block / a.cpr, (long long)cache::MAX_SLOTS, slots / 148}));
+  a.tpb = (int)std::max(1LL, std::min({(long long)per_block / a.cpr, (long long)cache::MAX_SLOTS, slots / n_sm}));
   a.index_err = index_err;
   const long long blocks = (slots + a.tpb - 1) / a.tpb;
   cache::append_kernel<<<(unsigned)blocks, cache::THREADS, 0, st>>>(a);

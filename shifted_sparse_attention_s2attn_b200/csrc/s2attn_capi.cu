@@ -806,10 +806,11 @@ int s2attn_cache_append(const void* k_new, const void* v_new, void* k_pages, voi
       !aligned4(cache_len) || (rows && !aligned4(rows)) || (n_rows && !aligned4(n_rows)))
     return S2ATTN_ERR_INVALID_ARG;
   int* err = error_word_ptr();
-  if (!err) return S2ATTN_ERR_CUDA;
+  const int n_sm = sm_count();
+  if (!err || n_sm <= 0) return S2ATTN_ERR_CUDA;
   return cuda_status(s2::launch_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, rows, n_rows, B, M,
-                                             A, table_width, n_pages, page_shift_of(page_size), (int)row_bytes, err + 1,
-                                             static_cast<cudaStream_t>(stream)));
+                                             A, table_width, n_pages, page_shift_of(page_size), (int)row_bytes, n_sm,
+                                             err + 1, static_cast<cudaStream_t>(stream)));
 }
 
 int s2attn_cache_copy_pages(void* const* pools, int n_pools, const int* pairs, int n_pairs, int n_pages,
