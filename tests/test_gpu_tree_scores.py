@@ -26,15 +26,16 @@ def _row(q, k, v, dt):
     s = (k.double() @ q.double()) / math.sqrt(D)
     keep = s > -math.inf
     if not keep.any():
-        return torch.zeros(D).double(), -math.inf, torch.zeros(D).double(), 0.0
+        z = torch.zeros(D).double()
+        return z, z[0] - math.inf, z, z[0]
     s, k, v = s[keep], k[keep].double(), v[keep].double()
     p = torch.exp(s - s.max())
     o, pv = (p @ v) / p.sum(), (p @ v.abs()) / p.sum()
-    lse = (s.max() + p.sum().log()).item()
+    lse = s.max() + p.sum().log()
     e = D * 2.0 ** -23 * ((k.abs() @ q.double().abs()).max() / math.sqrt(D)) + 2.0 ** -18
     u = HALF_STEP[dt]
     tiny = 2.0 ** -25 if dt is FP else 0.0
-    return o, lse, (u * o.abs() + (u + 2 * e) * pv + tiny * (1 + v.abs().sum(0))) * 1.02, e + 2.0 ** -18 * (1 + abs(lse))
+    return o, lse, (u * o.abs() + (u + 2 * e) * pv + tiny * (1 + v.abs().sum(0))) * 1.02, e + 2.0 ** -18 * (1 + lse.abs())
 
 
 def _check_rows(c, see, words, new):
@@ -53,8 +54,7 @@ def _check_rows(c, see, words, new):
                 wo, wl, bo, bl = _row(c["q"][b, m, h], torch.cat([kc, c["k_new"][b, on, g]]),
                                       torch.cat([vc, c["v_new"][b, on, g]]), c["q"].dtype)
                 check_close(o[b, m, h], wo, bo, f"o of sequence {b} token {m} head {h}")
-                check_close(lse[b, h, m], torch.tensor(wl, dtype=torch.float64), torch.tensor(bl, dtype=torch.float64),
-                            f"lse of sequence {b} token {m} head {h}")
+                check_close(lse[b, h, m], wl, bl, f"lse of sequence {b} token {m} head {h}")
 
 
 # 300 key heads leave one run a unit, a few heads one tile a run
