@@ -481,8 +481,9 @@ def _norm_rope_ref(q, k, names, norm, wq, wk, inv_freq, positions, pos0):
     if ref is None:
         raise ValueError(f"{names[0]} or {names[1]} must be given")
     shape, dtype, dev = ref.shape, ref.dtype, ref.get_device()
-    if len(shape) != 4 or shape[0] * shape[1] >= 2 ** 30:      # (the C call's sizes are 32-bit)
-        raise ValueError(f"{names[0]} and {names[1]} must be [B,N,H,D] with B*N below 2^30")
+    # (the C calls' sizes are 32-bit)
+    if len(shape) != 4 or shape[0] * shape[1] >= 2 ** 30 or shape[2] >= 2 ** 31 or shape[3] >= 2 ** 31:
+        raise ValueError(f"{names[0]} and {names[1]} must be [B,N,H,D] with B*N below 2^30, H and D below 2^31")
     if wq is not None:
         _fit(wq, "wq", shape[3:], dtype, dev)
     if wk is not None:
@@ -500,8 +501,8 @@ def _norm_rope_ref(q, k, names, norm, wq, wk, inv_freq, positions, pos0):
 
 
 def _norm_rope_k_shape(shape, k, name):
-    if k.dim() != 4:
-        raise ValueError(f"{name} must be [B,N,H,D]")
+    if k.dim() != 4 or k.shape[2] >= 2 ** 31:
+        raise ValueError(f"{name} must be [B,N,H,D] with H below 2^31")
     return shape[0], shape[1], k.shape[2], shape[3]
 
 
@@ -579,8 +580,8 @@ def s2attn_tree_mask(parents, mask, depth=None, stream=None):
     """Ancestor masks of trees of drafted tokens: parents [B,M] int32 (-1: follows the cache) ->
     mask [B,M,ceil(M/64)] int64 (bit j: j is m or an ancestor) and depth [B,M] int32."""
     torch = _torch()
-    if parents.dim() != 2:
-        raise ValueError("parents must be [B,M]")
+    if parents.dim() != 2 or parents.numel() >= 2 ** 31:
+        raise ValueError("parents must be [B,M] with fewer than 2^31 nodes")
     B, M = parents.shape
     dev = parents.get_device()
     _fit(parents, "parents", (B, M), torch.int32, dev)
@@ -624,6 +625,8 @@ def s2attn_tree_decode(q, k_new, v_new, k_pages, v_pages, page_table, cache_len,
         raise ValueError("q must be [B,M,H,D] and k_new [B,M,Hkv,D]")
     B, M, H, D = q.shape
     Hkv = k_new.shape[2]
+    if B >= 2 ** 31 or M >= 2 ** 31 or H >= 2 ** 31 or D >= 2 ** 31 or Hkv >= 2 ** 31:
+        raise ValueError("every size of q and k_new must be below 2^31")
     dtype, dev = q.dtype, q.get_device()
     code = _dtype_code(dtype, "q", False)
     _fit(q, "q", (B, M, H, D), dtype, dev)
@@ -650,8 +653,8 @@ def s2attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, r
     if k_new.dim() != 4:
         raise ValueError("k_new must be [B,M,Hkv,D]")
     B, M, Hkv, D = k_new.shape
-    if B * M >= 2 ** 30:
-        raise ValueError("k_new must have fewer than 2^30 rows")
+    if B * M >= 2 ** 30 or Hkv >= 2 ** 31 or D >= 2 ** 31:
+        raise ValueError("k_new must have fewer than 2^30 rows, and Hkv and D below 2^31")
     dtype, dev = k_new.dtype, k_new.get_device()
     _dtype_code(dtype, "k_new", True)
     _fit(k_new, "k_new", (B, M, Hkv, D), dtype, dev)
@@ -659,8 +662,8 @@ def s2attn_cache_append(k_new, v_new, k_pages, v_pages, page_table, cache_len, r
     n_pages, page_size, width = _paged(k_pages, v_pages, page_table, cache_len, B, Hkv, D, dtype, dev)
     A = M
     if rows is not None:
-        if rows.dim() != 2:
-            raise ValueError("rows must be [B,A]")
+        if rows.dim() != 2 or rows.numel() >= 2 ** 30:
+            raise ValueError("rows must be [B,A] with B*A below 2^30")
         A = rows.shape[1]
         _fit(rows, "rows", (B, A), torch.int32, dev)
     if n_rows is not None:

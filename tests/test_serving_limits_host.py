@@ -54,3 +54,36 @@ def test_copy_limit(lib, page_bytes, rc):
     import ctypes
     pools = (ctypes.c_void_p * 1)(P + 8)       # misaligned
     assert lib.s2attn_cache_copy_pages(pools, 1, (ctypes.c_int * 2)(0, 1), 1, 2, page_bytes, None) == rc
+
+
+def test_binding_refuses_every_size_past_32_bits():
+    """The C calls' sizes are 32-bit: one of 2^32 + x must not reach them as x.  Tensors without memory."""
+    import torch
+
+    def big(*shape, dtype=torch.bfloat16):
+        return torch.zeros(1, dtype=dtype).expand(*shape)
+    W = 2 ** 32 + 16
+    f, i32 = torch.zeros(8), torch.int32
+    calls = [
+        lambda: s2.qk_norm_rope_fwd(big(1, 1, W, 16), None, big(1, 1, W, 16), None, f),
+        lambda: s2.qk_norm_rope_fwd(None, big(1, 1, 4, W), None, big(1, 1, 4, W), f),
+        lambda: s2.qk_norm_rope_fwd(big(1, 1, 4, 16), big(1, 1, W, 16), big(1, 1, 4, 16), big(1, 1, W, 16), f),
+        lambda: s2.qk_norm_rope_bwd(None, None, big(1, 1, W, 16), None, big(1, 1, W, 16), None, f, norm=False),
+        lambda: s2.s2attn_tree_mask(big(W, 1, dtype=i32), big(W, 1, 1, dtype=torch.int64)),
+        lambda: s2.s2attn_tree_decode(big(W, 1, 1, 64), big(W, 1, 1, 64), big(W, 1, 1, 64), big(2, 16, 1, 64),
+                                      big(2, 16, 1, 64), big(W, 1, dtype=i32), big(W, dtype=i32), big(W, 1, 1, 64),
+                                      big(W, 1, 1, dtype=torch.float32), torch.zeros(1)),
+        lambda: s2.s2attn_tree_decode(big(1, 1, W, 64), big(1, 1, W, 64), big(1, 1, W, 64), big(2, 16, W, 64),
+                                      big(2, 16, W, 64), big(1, 1, dtype=i32), big(1, dtype=i32), big(1, 1, W, 64),
+                                      big(1, W, 1, dtype=torch.float32), torch.zeros(1)),
+        lambda: s2.s2attn_cache_append(big(1, 2, 1, W), big(1, 2, 1, W), big(2, 16, 1, W), big(2, 16, 1, W),
+                                       big(1, 1, dtype=i32), big(1, dtype=i32)),
+        lambda: s2.s2attn_cache_append(big(1, 2, W, 16), big(1, 2, W, 16), big(2, 16, W, 16), big(2, 16, W, 16),
+                                       big(1, 1, dtype=i32), big(1, dtype=i32)),
+        lambda: s2.s2attn_cache_append(big(1, 2, 1, 16), big(1, 2, 1, 16), big(2, 16, 1, 16), big(2, 16, 1, 16),
+                                       big(1, 1, dtype=i32), big(1, dtype=i32), rows=big(1, W, dtype=i32)),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="2\\^3[01]"):
+            call()
+            pytest.fail(f"call {i} was taken")
