@@ -3,9 +3,9 @@
 //
 // The copies are HBM-bound: each byte is read once and written once.  A thread moves four
 // 16-byte pieces (of K and of V, when appending) and has all loads in flight before the first
-// store.  Measured (B200): 32k tokens of 8 heads x 128 in bf16 appended in 43 us = 6.2 TB/s, 0.95
+// store.  Measured (B200): 32k tokens of 8 heads x 128 in bf16 appended in 43-46 us = 5.8-6.2 TB/s, 0.89-0.95
 // of the copy bandwidth (59 us when every piece looked its row up); 500 pages of 131 KB copied in
-// four pools in 84 us = 6.2 TB/s; 8 pages in 32 pools, and 32 sequences' accepted rows, in 3 us.
+// four pools in 84-90 us = 5.8-6.2 TB/s; 8 pages in 32 pools, and 32 sequences' accepted rows, in 3-4 us.
 #include <algorithm>
 
 #include "s2_internal.h"

@@ -21,8 +21,9 @@
 // dw: a thread keeps the sums of its 16 columns over all rows it takes, the CTA adds its
 // rows' threads in a fixed order and writes one partial; a second kernel adds the partials
 // in order, so dw does not depend on which CTA ran first.
-// Measured (B200, bf16, D = 128): forward of a 32k prompt, 32 + 32 heads, 183 us = 5.9 TB/s, 0.90 of
-// the copy bandwidth; forward and backward at 8k, 32 + 8 heads, 85 us, 4.9 TB/s.  Tried and not
+// Measured (B200, bf16, D = 128): forward of a 32k prompt, 32 + 32 heads, 182-195 us = 5.5-5.9 TB/s, 0.84-0.90
+// of the copy bandwidth; forward and backward at 8k, 32 + 8 heads, 84-90 us, 4.7-5.0 TB/s.  In fp32 395-400 us
+// (0.82) and 153-158 us (0.83); its instances spill (8 bytes forward, 20 backward).  Tried and not
 // kept: rows through a ring of bulk copies in shared memory (192 and 127 us), one chunk a lane with
 // the other half shuffled (237 and 125), kernels of their own for each layout and for rows with and
 // without the norm (181 and 90).

@@ -27,13 +27,16 @@
 //     from TMEM.  S and P V are issued by a warp each, so that S(i+1) runs as soon as P(i-1) V(i-1)
 //     has left its buffer, while the softmax works on S(i).  Two CTAs share an SM (256 TMEM
 //     columns and 106 KB of shared memory each).
-// Measured (B200, bf16, D = 128; bytes: K and V once; both kernels, back to back):
-//   one token, 32k cached, 32 + 32 heads      90 us   6.0 TB/s, 0.91 of the copy bandwidth
+// Measured (B200, bf16, D = 128; bytes: K and V once; both kernels; first back to back in a captured
+// graph, then as calls among other work with cold caches):
+//   one token, 32k cached, 32 + 32 heads      89-90 us, 0.91 of the copy bandwidth; 99-104 us, 0.79-0.83
 //   16 sequences of 100 to 16384 tokens, up to 32 drafted, 32 heads over 8, pages of 16
-//                                             66 us   4.1 TB/s; 12 us of start and join
-//   100k cached, 64 drafted, 64 heads over 8 207 us   1.04 PFLOP/s, 0.63 of the burst rate
-//   two chats of at most 300 tokens, D = 64   11 us   latency: start, one tile, join
-// The last but one is bound by the chain of a tile (S, row max, exponentials, P V): 128-key tiles
+//                                             65-66 us, 4.1-4.2 TB/s, 12 us of start and join; 72-75 us
+//   100k cached, 64 drafted, 64 heads over 8  207-211 us, 1.02-1.04 PFLOP/s, 0.62-0.63 of the burst rate;
+//                                             242-249 us, 0.86-0.89 PFLOP/s
+//   the same with D = 64                      179-187 us, 0.58-0.60 PFLOP/s
+//   two chats of at most 300 tokens, D = 64   12 us with their mask: start, one tile, join; 22-23 us
+// 100k is bound by the chain of a tile (S, row max, exponentials, P V): 128-key tiles
 // with one S buffer and four or eight softmax warps took 224 and 233 us where this took 226, and
 // a share of the exponentials on the FMA pipe (a quarter, a third, a half) 210, 212 and 224 where
 // this took 207.  Its N = 64 MMAs cost as much as N = 128 ones (A is read from shared memory at
@@ -66,7 +69,9 @@ static_assert(NTHREADS == 32 * (WARP_PV + 1), "four softmax warps, then these");
 constexpr uint32_t QBOX = BM * 128;          // 128 rows x 128 B (64 columns)
 constexpr uint32_t KBOX = BN * 128;
 constexpr int NBARS = 2 + 2 * KST + 2 * VST + 3 * 2 + 3 + 2;
-constexpr int kSeqCost = 3;                  // of a sequence's end, in key tiles
+// What a sequence's end costs, in key tiles.  With 1, 2, 3, 4, 5: two short chats 11.3, 12.0, 12.0, 12.3, 12.8 us;
+// the batch of 16 64.4, 65.2, 65.3, 64.9, 65.4; 256 sequences of up to 2000 tokens 119.9, 115.3, 110.7, 108.5, 109.5.
+constexpr int kSeqCost = 3;
 constexpr uint32_t TM_COLS = 256;
 constexpr uint32_t TM_O = 128;               // S buffers at columns 0 and 64
 
