@@ -210,7 +210,7 @@ int rope_pi_apply_offset(void* q, void* k, int B, int N, int H, int D, int pos0,
  * dtype: S2ATTN_BF16, S2ATTN_FP16 or S2ATTN_F32.  Sums and products are fp32, angles are formed and reduced in
  * 64 bits, the result is rounded once.  q_out == q and k_out == k (in place) are allowed; other overlaps are
  * not.  Requirements: D % 16 == 0, D <= 256; R % 16 == 0, 0 <= R <= D; Hq, Hk <= 16384; B * N < 2^30; pos0 + N
- * < 2^31; eps >= 0; device pointers 16-byte aligned (positions and inv_freq 4-byte).
+ * < 2^31; eps >= 0; a row's sum of squares within fp32; device pointers 16-byte aligned (positions and inv_freq 4-byte).
  */
 int qk_norm_rope_fwd(const void* q, const void* k, const void* wq, const void* wk, const int* positions,
                      const float* inv_freq, void* q_out, void* k_out, int B, int N, int Hq, int Hk, int D, int R,
@@ -222,7 +222,8 @@ int qk_norm_rope_fwd(const void* q, const void* k, const void* wq, const void* w
  * (either may be NULL: not wanted; both must be NULL when norm == 0).  dw is the fp32 sum over
  * all tokens and heads, added in an order that depends on the sizes and the device alone.
  * dq == dq_out and dk == dk_out are allowed.  `workspace`: device, 256-byte aligned, at
- * least qk_norm_rope_bwd_workspace_bytes(D) bytes; may be NULL when dwq and dwk are.
+ * least qk_norm_rope_bwd_workspace_bytes(D) bytes, one per call that may overlap on the GPU; may be NULL
+ * when dwq and dwk are.
  */
 size_t qk_norm_rope_bwd_workspace_bytes(int D);
 int qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out, const void* wq,
@@ -280,10 +281,11 @@ int s2attn_tree_mask(const int* parents, unsigned long long* mask, int* depth, i
  * whose bit is set in its mask row.  Rows m >= new_len[b] of o and lse are left as they were.  A token that
  * sees nothing gets o = 0 and lse = -inf.  What is not visible to a token does not reach it, whatever it holds
  * (infinities and NaN included).  A visible key of score -inf has weight 0; a token whose scores are all -inf
- * gets o = 0 and lse = -inf too. dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to
- * dtype for the second product (in fp16 what is below 2^-36 of a row's largest weight is lost there).
- * Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024, B * M * H < 2^31 and B *
- * (table_width * page_size / 64 + 16) < 2^30 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
+ * gets o = 0 and lse = -inf too.
+ * dtype: S2ATTN_BF16 or S2ATTN_FP16.  Scores and sums are fp32; P is rounded to dtype for the second product
+ * (in fp16 what is below 2^-36 of a row's largest weight is lost there).
+ * Requirements: Hkv divides H, H/Hkv <= 128; D 64 or 128, M <= 128, B <= 1024, B * M * H < 2^31 and
+ * B * (table_width * page_size / 64 + 16) < 2^30 (else S2ATTN_ERR_UNSUPPORTED).  `workspace` (device, 256-byte
  * aligned, at least s2attn_tree_decode_workspace_bytes bytes) is overwritten: calls that may overlap on the
  * GPU need one each.  Lengths are read on the device only, so a captured call follows them; they must not
  * change while it runs.  o and lse must not overlap the inputs.  Runs up to two kernels on `stream`.  Repeated
@@ -300,7 +302,7 @@ int s2attn_tree_decode(const void* q, const void* k_new, const void* v_new, cons
 /*
  * Writes rows of k_new and v_new ([B, M, Hkv, D]) into the pages of their sequences: for j < n_rows[b], row
  * rows[b][j] goes to position cache_len[b] + j.  rows [B, A] int32 (any order, repeats allowed); NULL: row j,
- * A = M.  n_rows [B] int32 (values above A count as A, below 0 as 0); NULL: A. cache_len is not changed.
+ * A = M.  n_rows [B] int32 (values above A count as A, below 0 as 0); NULL: A.  cache_len is not changed.
  * k_new and v_new must not overlap the pools.  elem_size: bytes of an element (2 or 4); Hkv * D * elem_size
  * must be a multiple of 16, at most 2^20, and B * M and B * A below 2^30 (else S2ATTN_ERR_UNSUPPORTED).  No
  * two sequences may own the same page at a position that is written.
